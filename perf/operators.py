@@ -186,8 +186,9 @@ def _plain_norm(s):
     r = (1.0 / (v.double().square().mean(1, keepdim=True) + s["eps"]).sqrt()).float()
     y = v * r * s["gain"]
     a = y.abs().amax(1, keepdim=True)
-    q = torch.where(a > 0, (y * (127.0 / a)).round().clamp(-127, 127), torch.zeros_like(y))
-    return out + [q.to(torch.int8), (a / 127.0)[:, 0]]
+    top = torch.full_like(a, 127.0)  # divisions are tensor by tensor: one by a number is a product with its reciprocal
+    q = torch.where(a > 0, (y * (top / a)).round().clamp(-127, 127), torch.zeros_like(y))
+    return out + [q.to(torch.int8), (a / top)[:, 0]]
 
 
 def _token_places(s):
@@ -208,7 +209,7 @@ def _rotate(x, cs):
 def _codes(x):
     """4-bit codes of the last axis and their fp16 scale and minimum."""
     lo, hi = x.amin(2, keepdim=True), x.amax(2, keepdim=True)
-    sc, mn = ((hi - lo) / 15.0).half(), lo.half()
+    sc, mn = ((hi - lo) / torch.full_like(lo, 15.0)).half(), lo.half()
     inv = torch.where(sc > 0, 1.0 / sc.float(), torch.zeros_like(lo))
     return ((x - mn.float()) * inv).round().clamp(0, 15).to(torch.uint8), sc, mn
 
