@@ -367,6 +367,154 @@ tern_status tern_decode_step(const tern_decode_model* model, int32_t pos, const 
                              int32_t first, int32_t last, const float* d_attn_in, float* d_trace, void* d_ws,
                              size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a step of more than one token: the layer of tern_decode_step
+ * (QORA-LLM-2B page, "SubLN Pattern (4 norms per layer)") for prompts and for
+ * batches of sequences. The ternary linears are tern_gemm_batched with
+ * TERN_ACT_INT8; around them stand the normalisation that produces its int8
+ * input, a paged cache of keys and values in 4 bits with the attention that
+ * reads it, and an 8-bit product for layers that are not ternary (the token
+ * head). The pages run one token at a time over an unquantised cache; the
+ * several-token forms, the 4-bit cache and the 8-bit product are this
+ * library's. Row strides (ld*) are in elements.
+ * ------------------------------------------------------------------------ */
+
+/* What tern_norm_quantize normalises: x; the residual sum x + r; or the gated
+ * activation relu(x)^2 * r ("max(0,x)^2" on the QORA-LLM-2B page). */
+typedef enum { TERN_NORM_PLAIN = 1, TERN_NORM_ADD = 2, TERN_NORM_RELU2 = 3 } tern_norm;
+
+/*
+ * RMSNorm of m rows of k values and its int8 quantisation per row, the input
+ * of TERN_ACT_INT8 products; every step in fp32 with one rounding each:
+ *   v = x                               (TERN_NORM_PLAIN)
+ *   v = x + r, rounded to r_type, written to d_sum        (TERN_NORM_ADD)
+ *   v = fl(fl(g g) r), g = max(x, 0)    (TERN_NORM_RELU2)
+ *   y_i = fl(fl(v_i f) gain_i), f = fl(1 / sqrt(mean(v^2) + eps)) (sum in fp64)
+ *   xq, xscale = the rule of tern_quantize_act on y
+ * the same values as the normalisations inside tern_decode_step. Inputs must be
+ * finite. m = 0 does nothing.
+ *   d_x [m][k] of x_type (TERN_OUT_F32 or TERN_OUT_BF16), row stride ldx >= k;
+ *   d_r [m][k] of r_type, ldr >= k (TERN_NORM_PLAIN: ignored);
+ *   d_gain fp32 [k]; eps > 0;
+ *   d_sum [m][k] of r_type, ldsum >= k (TERN_NORM_ADD only; d_r itself for an
+ *     update in place, with the same stride);
+ *   d_xq int8 [m][k], ldq >= k (tern_gemm_batched wants ldq = k, tern_gemm_i8 a
+ *     multiple of 16); d_xscale float [m].
+ * Any k and any stride; rows of k <= 16384 with k and the strides multiples of 4
+ * and 16-byte aligned pointers are read once. TERN_EALIGN: a pointer not aligned
+ * to its element.
+ */
+tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, tern_out x_type, const void* d_x, int64_t ldx,
+                               tern_out r_type, const void* d_r, int64_t ldr, const float* d_gain, float eps,
+                               void* d_sum, int64_t ldsum, int8_t* d_xq, int64_t ldq, float* d_xscale, void* stream);
+
+/*
+ * A paged cache of one layer's keys and values in 4 bits. A page holds page_size
+ * tokens of every kv head; the block of a page and head is contiguous,
+ *   [num_pages][kv_heads][ K codes [page_size][head_dim / 2]
+ *                        | V codes [page_size][head_dim / 2]
+ *                        | fp16 [page_size][4]: k scale, k min, v scale, v min ]
+ * page_size (head_dim + 8) bytes. The code of dimension d of a token is in bits
+ * 4 (d mod 2) .. + 3 of byte d div 2 and stands for min + scale * code. Each
+ * token and head has its own scales, for keys (after RoPE) and for values x:
+ *   min = fp16_rn(min x), scale = fp16_rn(fl(fl(max x - min x) / 15)),
+ *   code = clamp(rint(fl(fl(x - min) fl(1 / scale))), 0, 15); scale 0: code 0.
+ * Values must be finite and within the fp16 range (+-65504).
+ */
+typedef struct tern_kv4_cache {
+  int32_t kv_heads;   /* 1..1024 */
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t page_size;  /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages;  /* pages that d_pages holds, >= 1 */
+  void* d_pages;      /* 16-byte aligned, tern_kv4_cache_size bytes */
+} tern_kv4_cache;
+
+/*
+ * The new tokens of a step: sequence s has the rows d_start[s] .. d_start[s+1]-1
+ * of the token buffers and, with them, d_len[s] tokens in all, so its i-th new
+ * token is at position d_len[s] - (number of new tokens) + i. Rows from
+ * d_start[seqs] on belong to no sequence: no call reads or writes them.
+ * A new token whose position is negative is not stored, its query is zero and
+ * its attention output is zero. The lengths and the table are read by the
+ * kernels, so a captured launch follows what they hold when it is replayed; a
+ * sequence they describe wrongly (rows out of order or beyond `tokens`, more
+ * than max_new new tokens, a length above max_len or above what its table
+ * holds) is left out: nothing of it is stored and its outputs are not written.
+ * The tokens of a page outside the cache are left out: not stored, not attended
+ * to, read as zero. Both are reported by tern_device_error as TERN_EFORMAT.
+ */
+typedef struct tern_kv4_batch {
+  int32_t seqs;            /* sequences, 0 .. 65535 */
+  int32_t tokens;          /* rows of the token buffers */
+  int32_t max_new;         /* most new tokens of a sequence */
+  int32_t max_len;         /* largest length */
+  int32_t max_pages;       /* row stride of the table */
+  const int32_t* d_start;  /* [seqs + 1] */
+  const int32_t* d_len;    /* [seqs] */
+  const int32_t* d_table;  /* [seqs][max_pages]: page of the tokens page_size j .. page_size (j + 1) - 1 */
+} tern_kv4_batch;
+
+/* Bytes of the cache's pages. */
+tern_status tern_kv4_cache_size(const tern_kv4_cache* cache, size_t* bytes);
+
+/*
+ * Rotate the new tokens' queries and keys and append keys and values to the
+ * cache, in one launch. RoPE as in tern_decode_step (rotate_half, every product
+ * and sum rounded in fp32).
+ *   d_q [tokens][heads * head_dim], d_k and d_v [tokens][kv_heads * head_dim] of
+ *     `type` (TERN_OUT_F32 or TERN_OUT_BF16), 16-byte aligned, row strides
+ *     multiples of 8 elements; d_q may be NULL with heads = 0 (keys and values only);
+ *   d_rope fp32 [max_pos][head_dim / 2][2] (tern_decode_rope_table), 16-byte
+ *     aligned; a position >= max_pos is an error like a bad page;
+ *   d_q_out bf16 [tokens][heads * head_dim], 16-byte aligned.
+ * No two tokens of a call may have the same place in the cache.
+ */
+tern_status tern_kv4_append(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, tern_out type,
+                            const void* d_q, int64_t ldq, const void* d_k, int64_t ldk, const void* d_v, int64_t ldv,
+                            const float* d_rope, int32_t max_pos, uint16_t* d_q_out, void* stream);
+
+/*
+ * The values that the cache holds for the batch's tokens (to read a whole
+ * sequence, let all its tokens be "new"): d_k, d_v [tokens][kv_heads * head_dim]
+ * of `type`, 16-byte aligned, row strides multiples of 8 elements; either may be
+ * NULL. fl(min + scale * code), zero for negative positions and bad pages.
+ */
+tern_status tern_kv4_read(const tern_kv4_cache* cache, const tern_kv4_batch* batch, tern_out type, void* d_k,
+                          int64_t ldk, void* d_v, int64_t ldv, void* stream);
+
+/* Workspace of tern_kv4_attention for batches of up to `seqs` sequences, max_new
+ * new tokens and max_len positions each: 256-byte aligned, zero-filled before
+ * its first use and left ready for the next call. Calls that may run at the same
+ * time need separate workspaces. */
+tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32_t seqs, int32_t max_new,
+                                              int32_t max_len, int32_t heads, size_t* bytes);
+
+/*
+ * Causal attention of the batch's new tokens over the cache (which holds them
+ * already): out = softmax(scale q k^T) v over the positions up to the token's
+ * own. Query head h reads kv head h / (heads / kv_heads); heads is a multiple of
+ * kv_heads, any ratio. Products on bf16 operands with fp32 accumulation (codes
+ * are exact in bf16; probabilities times value scales are rounded to bf16), the
+ * softmax in fp32.
+ *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.
+ */
+tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, float scale,
+                               const uint16_t* d_q, uint16_t* d_out, void* d_ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit product with a scale per token and per output channel, for the linears
+ * that are not ternary (the token head):
+ *   y[m][n] = fl(fl(fl(acc) d_wscale[n]) d_xscale[m]), acc = sum_k w[n][k] x[m][k]
+ * with acc the exact integer; rounded once more for TERN_OUT_BF16.
+ * tern_quantize_act on a weight matrix [n][k] gives d_w and d_wscale.
+ *   d_x int8 [m][k], d_w int8 [n][k]: 16-byte aligned, row strides ldx, ldw >= k
+ *   and multiples of 16 (bytes from k on are not used); k <= 131071;
+ *   d_y [m][n], row stride ldy >= n. m = 0 does nothing.
+ */
+tern_status tern_gemm_i8(int32_t m, int32_t n, int32_t k, const int8_t* d_x, int64_t ldx, const float* d_xscale,
+                         const int8_t* d_w, int64_t ldw, const float* d_wscale, tern_out out, void* d_y, int64_t ldy,
+                         void* stream);
+
 /*
  * Failure-detection self-test (the pages have no counterpart). Enqueues one
  * small kernel whose bounded wait cannot succeed: it waits on a shared-memory

@@ -486,6 +486,9 @@ tern_status run_single(const tern_desc* desc, const Layout& L, const void* d_pac
 }
 
 }  // namespace
+
+int sm_count() { return device_sms(); }
+
 }  // namespace tern
 
 using namespace tern;
@@ -641,6 +644,9 @@ extern "C" tern_status tern_device_error(void* stream) {
   if (read_clear_dev_error_gemm_tc(stream, &v) != 0) return TERN_ECUDA;
   if (read_clear_dev_error_selftest(stream, &v) != 0) return TERN_ECUDA;
   if (read_clear_dev_error_decode(stream, &v) != 0) return TERN_ECUDA;
+  if (read_clear_dev_error_kv4(stream, &v) != 0) return TERN_ECUDA;
+  if (read_clear_dev_error_kv4_attn(stream, &v) != 0) return TERN_ECUDA;
+  if (read_clear_dev_error_gemm_i8(stream, &v) != 0) return TERN_ECUDA;
   if (v & TERN_DEVERR_TIMEOUT) return TERN_ETIMEOUT;
   return v ? TERN_EFORMAT : TERN_OK;
 }

@@ -301,6 +301,90 @@ size_t decode_smem_bytes(const DecParams& p);
 int decode_ring_slots(const DecParams& p);
 int read_clear_dev_error_decode(void* stream, unsigned* out);
 
+// --------------------------------- operators of a step of many tokens
+struct NormParams {
+  const void* x;
+  const void* r;
+  const float* gain;
+  void* sum;
+  int8_t* xq;
+  float* xscale;
+  int64_t ldx, ldr, ldsum, ldq;
+  int m, k, mode, x_bf16, r_bf16;
+  float eps;
+};
+int launch_norm(const NormParams& p, void* stream);
+
+// The 4-bit cache and the batch as the kernels take them.
+struct Kv4Params {
+  uint8_t* pages;
+  const int32_t* start;
+  const int32_t* len;
+  const int32_t* table;
+  int kv_heads, dim, page, log_page, num_pages;
+  int seqs, tokens, max_new, max_len, max_pages;
+  int heads;
+};
+// Bytes of one (page, kv head) block; codes of K, codes of V, then fp16 [page][4].
+TERN_HD inline size_t kv4_block_bytes(int page, int dim) { return (size_t)page * (size_t)(dim + 8); }
+
+struct Kv4AppendParams {
+  Kv4Params c;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* rope;
+  uint16_t* q_out;
+  int64_t ldq, ldk, ldv;
+  int max_pos, bf16;
+};
+int launch_kv4_append(const Kv4AppendParams& p, void* stream);
+
+struct Kv4ReadParams {
+  Kv4Params c;
+  void* k;
+  void* v;
+  int64_t ldk, ldv;
+  int bf16;
+};
+int launch_kv4_read(const Kv4ReadParams& p, void* stream);
+int read_clear_dev_error_kv4(void* stream, unsigned* out);
+
+// Launch plan of the attention over few query rows: `rows` query rows per CTA
+// (8, 16 or 32), `tiles` row tiles per (sequence, kv head), positions split in
+// chunks of `chunk`, `splits` of them at the batch's largest length.
+struct Kv4AttnPlan {
+  int rows, tiles, chunk, splits;
+  long long units;            // (sequence, kv head, row tile)
+  size_t cnt_bytes, ws_bytes;
+};
+struct Kv4AttnParams {
+  Kv4Params c;
+  const uint16_t* q;
+  uint16_t* out;
+  float scale_log2;           // scale * log2(e)
+  int group;                  // query heads per kv head
+  int tiles, chunk, splits;
+  unsigned* cnt;              // [units], zero on entry and exit
+  float* part;                // [units][splits][rows][dim + 2]
+};
+int launch_kv4_attn(const Kv4AttnParams& p, const Kv4AttnPlan& plan, void* stream);
+int read_clear_dev_error_kv4_attn(void* stream, unsigned* out);
+
+struct GemmI8Params {
+  const int8_t* x;
+  const int8_t* w;
+  const float* xscale;
+  const float* wscale;
+  void* y;
+  int64_t ldx, ldw, ldy;
+  int m, n, k, out_bf16;
+};
+int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream);
+int read_clear_dev_error_gemm_i8(void* stream, unsigned* out);
+
+int sm_count();  // multiprocessors of the current device
+
 // Shared-memory bytes a 2-bit GEMV CTA needs for these parameters.
 size_t gemv2_smem_bytes(const Gemv2Params& p, int xmode);
 int gemv2_mt(int xmode, int m);   // tokens per pass of the kernel instantiated for m

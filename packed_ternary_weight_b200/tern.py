@@ -17,6 +17,7 @@ OK, EINVAL, EFORMAT, EALIGN, ENOSPACE, EUNSUPPORTED, ECUDA, ETIMEOUT = range(8)
 FMT = {"bitnet": 1, "tq": 2, "bt3": 3}
 ACT_INT8, ACT_BF16, ACT_BF16_Q8 = 1, 2, 3
 OUT_F32, OUT_BF16 = 1, 2
+NORM_PLAIN, NORM_ADD, NORM_RELU2 = 1, 2, 3
 F_PDL = 1
 
 
@@ -78,6 +79,32 @@ for _f in (lib.tern_decode_rope_table, lib.tern_decode_workspace_size, lib.tern_
 for _f in (lib.tern_selftest_wait, lib.tern_fit_tq, lib.tern_fit_bt, lib.tern_packed_size, lib.tern_pack, lib.tern_workspace_size, lib.tern_quantize_act, lib.tern_gemv,
            lib.tern_gemm_batched, lib.tern_device_error, lib.tern_gemv_noalloc, lib.tern_gemv_grouped,
            lib.tern_stream_read):
+    _f.restype = ctypes.c_int
+
+
+class KV4CacheC(ctypes.Structure):
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("d_pages", _vp)]
+
+
+class KV4BatchC(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("d_start", _vp), ("d_len", _vp),
+                ("d_table", _vp)]
+
+
+_i32, _i64, _cache_p, _batch_p = ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(KV4CacheC), ctypes.POINTER(KV4BatchC)
+lib.tern_norm_quantize.argtypes = [ctypes.c_int, _i32, _i32, ctypes.c_int, _vp, _i64, ctypes.c_int, _vp, _i64, _vp,
+                                   ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp]
+lib.tern_kv4_cache_size.argtypes = [_cache_p, ctypes.POINTER(_sz)]
+lib.tern_kv4_append.argtypes = [_cache_p, _batch_p, _i32, ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32,
+                                _vp, _vp]
+lib.tern_kv4_read.argtypes = [_cache_p, _batch_p, ctypes.c_int, _vp, _i64, _vp, _i64, _vp]
+lib.tern_kv4_attention_workspace_size.argtypes = [_cache_p, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]
+lib.tern_kv4_attention.argtypes = [_cache_p, _batch_p, _i32, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]
+lib.tern_gemm_i8.argtypes = [_i32, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _vp, _i64, _vp]
+for _f in (lib.tern_norm_quantize, lib.tern_kv4_cache_size, lib.tern_kv4_append, lib.tern_kv4_read,
+           lib.tern_kv4_attention_workspace_size, lib.tern_kv4_attention, lib.tern_gemm_i8):
     _f.restype = ctypes.c_int
 
 
@@ -254,3 +281,181 @@ def fit_bt(w, depth: int, codebook, trits, idx, stream=None):
     n, k = w.shape
     _check(lib.tern_fit_bt(_ptr(w), n, k, depth, _ptr(codebook), _ptr(trits), _ptr(idx), _stream(stream)),
            "tern_fit_bt")
+
+
+def _type(t, what: str) -> int:
+    """TERN_OUT_* of a float tensor."""
+    name = str(t.dtype)
+    if name == "torch.float32":
+        return OUT_F32
+    if name == "torch.bfloat16":
+        return OUT_BF16
+    raise TernError(EINVAL, f"{what}: {name} is neither float32 nor bfloat16")
+
+
+def _want(ok: bool, what: str):
+    if not ok:
+        raise TernError(EINVAL, what)
+
+
+def _rows(t, m: int, k: int, what: str) -> int:
+    """Row stride of a tensor [m][k] whose rows are contiguous."""
+    _want(t.dim() == 2 and t.shape[0] == m and t.shape[1] == k and (k == 1 or t.stride(1) == 1), what)
+    return t.stride(0) if m > 1 else max(k, t.stride(0))
+
+
+def _vector(t, n: int, name: str, what: str):
+    _want(str(t.dtype) == name and t.numel() == n and t.is_contiguous(), what)
+
+
+def _launch(dev, stream, what: str, fn, *args):
+    """Call an entry point on the device that the tensors are on."""
+    import torch
+    _want(dev.type == "cuda", f"{what}: tensors are not on a CUDA device")
+    if dev.index == torch.cuda.current_device():
+        return _check(fn(*args, _stream(stream)), what)
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(stream)), what)
+
+
+def norm_quantize(mode: int, x, r, gain, eps: float, sum, xq, xscale, stream=None):
+    """RMSNorm of x (NORM_PLAIN), of x + r, which goes to `sum` (NORM_ADD), or of relu(x)^2 r (NORM_RELU2), quantised
+    to int8 per row: x, r, sum [m][k] float32 or bfloat16 (sum of r's type, or r itself), gain float32 [k], xq int8
+    [m][k], xscale float32 [m]."""
+    what = "tern_norm_quantize"
+    m, k = x.shape
+    two, add = mode != NORM_PLAIN, mode == NORM_ADD
+    _want(not two or r is not None, f"{what}: r is missing")
+    _want(not add or (sum is not None and sum.dtype == r.dtype), f"{what}: sum has r's type")
+    _vector(gain, k, "torch.float32", f"{what}: gain")
+    _vector(xscale, m, "torch.float32", f"{what}: xscale")
+    _want(str(xq.dtype) == "torch.int8", f"{what}: xq is int8")
+    dev = x.device
+    _want(gain.device == dev and xq.device == dev and xscale.device == dev and (not two or r.device == dev) and
+          (not add or sum.device == dev), f"{what}: tensors on several devices")
+    _launch(dev, stream, what, lib.tern_norm_quantize, mode, m, k, _type(x, what), x.data_ptr(),
+            _rows(x, m, k, f"{what}: x"), _type(r, what) if two else 0, r.data_ptr() if two else None,
+            _rows(r, m, k, f"{what}: r") if two else 0, gain.data_ptr(), eps, sum.data_ptr() if add else None,
+            _rows(sum, m, k, f"{what}: sum") if add else 0, xq.data_ptr(), _rows(xq, m, k, f"{what}: xq"),
+            xscale.data_ptr())
+
+
+def gemm_i8(x, xscale, w, wscale, y, stream=None):
+    """y[m][n] = x[m][k] w[n][k]^T with a scale per row of x and of w: x, w int8 (row strides multiples of 16), xscale
+    float32 [m], wscale float32 [n], y float32 or bfloat16."""
+    what = "tern_gemm_i8"
+    m, k = x.shape
+    n = w.shape[0]
+    _want(str(x.dtype) == "torch.int8" and str(w.dtype) == "torch.int8", f"{what}: x and w are int8")
+    _vector(xscale, m, "torch.float32", f"{what}: xscale")
+    _vector(wscale, n, "torch.float32", f"{what}: wscale")
+    dev = x.device
+    _want(w.device == dev and xscale.device == dev and wscale.device == dev and y.device == dev,
+          f"{what}: tensors on several devices")
+    ldx, ldw = _rows(x, m, k, f"{what}: x"), _rows(w, n, k, f"{what}: w")
+    if m <= 1:
+        ldx = (ldx + 15) & ~15  # the stride of a single row is free
+    if n <= 1:
+        ldw = (ldw + 15) & ~15
+    _launch(dev, stream, what, lib.tern_gemm_i8, m, n, k, x.data_ptr(), ldx, xscale.data_ptr(), w.data_ptr(), ldw,
+            wscale.data_ptr(), _type(y, what), y.data_ptr(), _rows(y, m, n, f"{what}: y"))
+
+
+class KV4Batch:
+    """Marshalled tern_kv4_batch: start int32 [seqs + 1], len int32 [seqs] and table int32 [seqs][max_pages] on the
+    device; tokens, max_new and max_len are host bounds that the launches are planned with."""
+
+    def __init__(self, start, len, table, tokens: int, max_new: int, max_len: int):
+        what = "tern_kv4_batch"
+        seqs = start.numel() - 1
+        _vector(start, seqs + 1, "torch.int32", f"{what}: start")
+        _vector(len, seqs, "torch.int32", f"{what}: len")
+        _want(table.dim() == 2 and table.shape[0] == seqs, f"{what}: table")
+        _vector(table, table.numel(), "torch.int32", f"{what}: table")
+        _want(len.device == start.device and table.device == start.device, f"{what}: tensors on several devices")
+        self._keep = (start, len, table)
+        self.device, self.tokens = start.device, tokens
+        self.c = KV4BatchC(seqs, tokens, max_new, max_len, table.shape[1], start.data_ptr(), len.data_ptr(),
+                           table.data_ptr())
+
+
+class KV4Cache:
+    """Marshalled tern_kv4_cache: `pages` is a contiguous uint8 tensor of whole pages, owned by the caller."""
+
+    def __init__(self, pages, kv_heads: int, head_dim: int, page_size: int):
+        what = "tern_kv4_cache"
+        _want(str(pages.dtype) == "torch.uint8" and pages.is_contiguous(), f"{what}: pages is contiguous uint8")
+        page_bytes = kv_heads * page_size * (head_dim + 8)
+        _want(page_bytes > 0 and pages.numel() % page_bytes == 0, f"{what}: pages holds whole pages")
+        self._keep, self.device = pages, pages.device
+        self.kv_heads, self.head_dim = kv_heads, head_dim
+        self.c = KV4CacheC(kv_heads, head_dim, page_size, pages.numel() // page_bytes, pages.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def size(kv_heads: int, head_dim: int, page_size: int, num_pages: int) -> int:
+        """Bytes of a cache of num_pages pages."""
+        out = _sz()
+        c = KV4CacheC(kv_heads, head_dim, page_size, num_pages, None)
+        _check(lib.tern_kv4_cache_size(ctypes.byref(c), ctypes.byref(out)), "tern_kv4_cache_size")
+        return out.value
+
+    def _heads(self, t, tokens: int, what: str):
+        """Heads and row stride of a token buffer [tokens][heads * head_dim]."""
+        _want(t.device == self.device, f"{what}: tensors on several devices")
+        _want(t.dim() == 2 and t.shape[1] % self.head_dim == 0, what)
+        return t.shape[1] // self.head_dim, _rows(t, tokens, t.shape[1], what)
+
+    def append(self, batch: KV4Batch, q, k, v, rope, q_out, stream=None):
+        """Rotate q and k by position, store k and v. q [tokens][heads * head_dim] and q_out (bfloat16, contiguous)
+        may both be None; q, k, v are float32 or bfloat16, rope is the float32 table of decode_rope_table."""
+        what = "tern_kv4_append"
+        n = batch.tokens
+        heads, ldq = (0, 0) if q is None else self._heads(q, n, f"{what}: q")
+        hk, ldk = self._heads(k, n, f"{what}: k")
+        hv, ldv = self._heads(v, n, f"{what}: v")
+        _want(hk == self.kv_heads and hv == hk, f"{what}: k and v have the cache's heads")
+        _want(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), f"{what}: q, k and v have one type")
+        if q is not None:
+            _want(q_out is not None and q_out.device == self.device, f"{what}: q_out")
+            _vector(q_out, n * heads * self.head_dim, "torch.bfloat16", f"{what}: q_out")
+        _want(rope.dim() == 3 and rope.shape[1] * 2 == self.head_dim and rope.shape[2] == 2 and
+              rope.device == self.device and batch.device == self.device, f"{what}: rope")
+        _vector(rope, rope.numel(), "torch.float32", f"{what}: rope")
+        _launch(self.device, stream, what, lib.tern_kv4_append, self._ref, ctypes.byref(batch.c), heads,
+                _type(k, what), None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                rope.data_ptr(), rope.shape[0], None if q is None else q_out.data_ptr())
+
+    def read(self, batch: KV4Batch, k, v, stream=None):
+        """The cached keys and values of the batch's tokens into k and v [tokens][kv_heads * head_dim] (one may be
+        None), float32 or bfloat16."""
+        what = "tern_kv4_read"
+        _want(k is not None or v is not None, f"{what}: neither k nor v")
+        hk, ldk = (self.kv_heads, 0) if k is None else self._heads(k, batch.tokens, f"{what}: k")
+        hv, ldv = (self.kv_heads, 0) if v is None else self._heads(v, batch.tokens, f"{what}: v")
+        _want(hk == self.kv_heads and hv == hk, f"{what}: k and v have the cache's heads")
+        _want(k is None or v is None or k.dtype == v.dtype, f"{what}: k and v have one type")
+        _want(batch.device == self.device, f"{what}: tensors on several devices")
+        _launch(self.device, stream, what, lib.tern_kv4_read, self._ref, ctypes.byref(batch.c),
+                _type(v if k is None else k, what), None if k is None else k.data_ptr(), ldk,
+                None if v is None else v.data_ptr(), ldv)
+
+    def attention_workspace_size(self, seqs: int, max_new: int, max_len: int, heads: int) -> int:
+        out = _sz()
+        _check(lib.tern_kv4_attention_workspace_size(self._ref, seqs, max_new, max_len, heads, ctypes.byref(out)),
+               "tern_kv4_attention_workspace_size")
+        return out.value
+
+    def attention(self, batch: KV4Batch, q, scale: float, out, ws=None, stream=None):
+        """Causal attention of the batch's new tokens over the cache: q, out bfloat16 [tokens][heads * head_dim]
+        contiguous (out may be q); ws uint8, zero before its first use (attention_workspace_size)."""
+        what = "tern_kv4_attention"
+        _want(q.dim() == 2 and q.shape[1] % self.head_dim == 0 and batch.device == self.device and
+              q.device == self.device and out.device == self.device and (ws is None or ws.device == self.device),
+              f"{what}: q")
+        heads = q.shape[1] // self.head_dim
+        _vector(q, batch.tokens * q.shape[1], "torch.bfloat16", f"{what}: q")
+        _vector(out, q.numel(), "torch.bfloat16", f"{what}: out")
+        _launch(self.device, stream, what, lib.tern_kv4_attention, self._ref, ctypes.byref(batch.c), heads, scale,
+                q.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel() * ws.element_size())
