@@ -493,9 +493,10 @@ tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32
  * Causal attention of the batch's new tokens over the cache (which holds them
  * already): out = softmax(scale q k^T) v over the positions up to the token's
  * own. Query head h reads kv head h / (heads / kv_heads); heads is a multiple of
- * kv_heads, any ratio. Products on bf16 operands with fp32 accumulation (codes
- * are exact in bf16; probabilities times value scales are rounded to bf16), the
- * softmax in fp32.
+ * kv_heads, any ratio. Products on fp16 operands with fp32 accumulation: codes
+ * are exact, q keeps every element within 2^38 of its row's largest,
+ * probabilities times value scales are rounded to fp16; the softmax in fp32.
+ * Scores must be finite in fp32.
  *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.
  */
 tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, float scale,

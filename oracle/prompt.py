@@ -105,10 +105,10 @@ class Cache:
 def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np.ndarray):
     """Outputs fp64 [tokens][heads][d] and a bound on how far the kernel's may be from them.
 
-    The bound adds up: the bf16 rounding of the output, half a step 2^-8 of its value; the bf16 rounding of each
-    probability times value scale, which weighs the code: 2^-8 sum p s c; the fp32 accumulation of products with
-    128 + c (at most 143), a few roundings of 2^-23 (the tensor cores may cut instead of round) of the sum of
-    magnitudes; and the same in the scores, whose error d in the exponent changes every probability by d."""
+    The bound adds up: the bf16 rounding of the output, half a step 2^-8 of its value; the fp16 rounding of each
+    probability times value scale, which weighs the code: 2^-11 sum p s c; and the fp32 accumulation, a few roundings
+    of 2^-23 (the tensor cores may cut instead of round) of the sums of magnitudes, here and in the scores, whose
+    error d in the exponent changes every probability by d."""
     d, kvh = cache.d, cache.kvh
     g = heads // kvh
     out = np.zeros((q.shape[0], heads, d))
@@ -133,11 +133,11 @@ def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np
                     p /= p.sum()
                     o = p @ v[:seen]
                     out[starts[s] + i, h * g + e] = o
-                    mag = abs(scale) * np.abs(qi).sum() * (143 * ks[:seen] + np.abs(km[:seen])).max()
+                    mag = abs(scale) * np.abs(qi).sum() * (15 * ks[:seen] + np.abs(km[:seen])).max()
                     err = 2.0 ** -20 * (mag + np.abs(sc).max() + 1)
-                    rest = (p @ (np.abs(vm[:seen]) + 143 * vs[:seen]))
-                    tol[starts[s] + i, h * g + e] = (2.0 ** -8 * (np.abs(o) + p @ (vs[:seen, None] * vc[:seen])) * 1.01
-                                                     + 2 * err * (p @ np.abs(v[:seen]) + np.abs(o)) + 2.0 ** -20 * rest)
+                    terms = p @ (np.abs(vm[:seen, None]) + vs[:seen, None] * vc[:seen])
+                    tol[starts[s] + i, h * g + e] = (2.0 ** -8 * np.abs(o) + 1.01 * 2.0 ** -11 * (p @ (vs[:seen, None] * vc[:seen]))
+                                                     + 2 * err * (p @ np.abs(v[:seen]) + np.abs(o)) + 2.0 ** -20 * terms)
     return out, tol
 
 

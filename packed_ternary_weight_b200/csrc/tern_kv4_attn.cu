@@ -5,29 +5,43 @@
 // (s, m) per token and head, so q k = s (q c) + m sum(q): the tensor cores
 // multiply q by the codes alone and the scales enter once per score. In the
 // same way sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j m_j, where the second
-// sum is one number per query row. A code becomes a bf16 operand with one
-// logic operation: the bit pattern 0x4300 | c is the bf16 number 128 + c, and
-// the 128s leave by 128 sum(q) per score and 128 sum_j bf16(p_j s_j) per row.
-// Softmax in base 2 with a running maximum; sums and statistics in fp32. The
-// probabilities times value scales are rounded to bf16 (half a step, 2^-9
-// relative, is below the bf16 rounding of the output), and the 128 sum uses the
-// rounded ones.
+// sum is one number per query row. Softmax in base 2 with a running maximum;
+// sums and statistics in fp32.
+//
+// Operands are fp16. A code needs no conversion: the four bits at the bottom of
+// an fp16 are the subnormal c 2^-24, and at bits 4-7 c 2^-20, both exact
+// operands, so one mask per two codes makes them (and a shift by 8 per four);
+// the factors 2^24 and 2^20 are powers of two that go into q and into the
+// output. q is bf16: its row is multiplied by a power of two that puts its
+// largest element at 2^14..2^15, so that its 8 significant bits fit for every
+// element within 2^38 of the largest. The weights p_j s_j are rounded to fp16 (half a step, 2^-11
+// relative; bf16 weights would add an error three times the output's own
+// rounding), scaled by a power of two that follows the largest s seen so far, so
+// that the largest is near 2^14 and small ones keep their bits.
 //
 // Layout. The scores are computed transposed, tokens x query rows
 // (m16n8k16): sixteen tokens of codes fill the A operand and eight query rows
 // the B operand, so one sequence's group of up to eight heads costs no padding
 // in the large dimension. The contraction may run over the dimensions in any
-// order, so lane 4 r + t takes the D/4 consecutive dimensions of token r that
-// are one 16-byte load (D = 128), and q is loaded in the same order. The
-// second product is transposed too, dimensions x rows: its A operand pairs the
-// same dimension of two tokens by byte permutation, and its B operand is the
-// bf16 probability matrix transposed in registers by movmatrix.
+// order, so lane 4 r + t takes D/4 consecutive dimensions of a token, 16 bytes
+// at D = 128, and q is loaded in the same order. The second product is
+// transposed too, dimensions x rows: its A operand pairs the same dimension of
+// two tokens by byte permutation, and its B operand is the probability matrix
+// transposed in registers by movmatrix. Row x of a score block stands for token
+// (x >> 1) + 4 (x & 1), which puts the tokens that four lanes read together in
+// the second product next to one another.
+//
+// Memory. Each warp has a ring of its own of three stages of 32 tokens, filled
+// by 16-byte asynchronous copies two stages ahead; 16 warps per multiprocessor
+// hold 139 KB in flight. The stage is swizzled in 16-byte pieces so that both
+// products read it without bank conflicts.
 //
 // Split. A CTA takes (sequence, kv head, tile of query rows, chunk of
 // positions); its eight warps take 32 positions in turn with softmax states of
 // their own, joined in shared memory. Chunks of one tile are joined by the last
 // CTA to arrive, in chunk order, so results do not depend on timing.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,16 +57,17 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;  // positions a warp takes at a time
+constexpr int kStep = 32;   // positions a warp takes at a time
+constexpr int kStages = 3;  // of its ring
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -62,35 +77,60 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
 }
-// Codes at bits 4 I .. + 3 of both halves as the bf16 pair 128 + c.
-template <int I>
-__device__ __forceinline__ uint32_t codes(uint32_t w) {
-  return ((w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
-}
 __device__ __forceinline__ uint32_t lo16(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t hi16(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+__device__ __forceinline__ uint32_t even4(uint32_t w) { return w & 0x000F000Fu; }  // codes at bits 0-3: c 2^-24
+__device__ __forceinline__ uint32_t odd4(uint32_t w) { return w & 0x00F000F0u; }   // codes at bits 4-7: c 2^-20
 __device__ __forceinline__ float2 half2_at(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where piece `c` (16 bytes) of token j's codes stands within a group of 16 tokens.
+template <int D>
+__device__ __forceinline__ uint32_t piece(int j, int c) {
+  if constexpr (D == 128) return (uint32_t)((j >> 1) * 128 + (((((j & 1) << 2) | c) ^ (j & 6)) << 4));
+  return (uint32_t)((j >> 2) * 128 + (((((j & 3) << 1) | c) ^ (j & 4)) << 4));
+}
+template <int D>
+struct Group {
+  static constexpr int kCodes = 16 * D / 2;           // bytes of 16 tokens' codes (keys or values)
+  static constexpr int kBytes = 2 * kCodes + 16 * 8;  // and their scale pairs
+};
 
 template <int WORDS>
-__device__ __forceinline__ void ldg_words(uint32_t (&v)[WORDS], const uint8_t* p) {
-  if constexpr (WORDS == 4) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-  } else if constexpr (WORDS == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    v[0] = u.x, v[1] = u.y;
-  } else {
-    v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
+__device__ __forceinline__ void lds_words(uint32_t (&v)[WORDS], uint32_t a) {
+  if constexpr (WORDS == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+  else if constexpr (WORDS == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a));
 }
 
 template <int D, int NT>
 struct Shared {
   static constexpr int kRows = 8 * NT, kPitch = D + 4;
-  float m[kWarps][kRows], l[kWarps][kRows];
-  float o[kWarps][kRows][kPitch];
+  union {
+    uint8_t ring[kWarps][kStages][2 * Group<D>::kBytes];
+    struct {
+      float m[kWarps][kRows], l[kWarps][kRows];
+      float o[kWarps][kRows][kPitch];
+    };
+  };
   int last;
 };
 
@@ -108,12 +148,13 @@ struct Join {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const Kv4AttnParams p) {
   constexpr int R = 8 * NT;          // query rows of the tile
   constexpr int KW = D / 32;         // words of K codes per lane and token
   constexpr int VW = D / 64;         // words of V codes per lane and token
   constexpr int MT = D / 16;         // 16-dimension tiles of the output
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  constexpr int CH = D / 32;         // 16-byte pieces of a token's codes
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   Shared<D, NT>& sm = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
   const Kv4Params& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
@@ -132,38 +173,103 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
   const int ns = limit_max > 0 ? (limit_max + p.chunk - 1) / p.chunk : 1;
   if (sp >= ns) return;
   const int begin = sp * p.chunk, end = min(limit_max, begin + p.chunk);
+  const size_t vofs = (size_t)c.page * (D / 2), pofs = (size_t)c.page * D;
 
-  // q in the order of the key words; sums of its rows
+  // the warp's steps: pages are looked up one step before their copies are issued
+  int pg[2];
+  auto look_up = [&](int t0) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int pos = t0 + 16 * g;
+      pg[g] = -1;
+      if (pos < end) {  // the same in all lanes
+        pg[g] = kv4::page_of(c, s, pos);
+        if (pg[g] < 0 && lane == 0) kv4::report_bad();
+      }
+    }
+  };
+  const uint32_t ring = smem_u32(sm.ring[warp]);
+  // copies of the step at t0 into a stage; returns which of its groups are there
+  auto issue = [&](int t0, int stage) {
+    uint32_t there = 0;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (pg[g] >= 0) {
+        there |= 1u << g;
+        const int slot = (t0 + 16 * g) & (c.page - 1);
+        const uint8_t* blk = c.pages + kv4::block_offset(c, pg[g], h);
+        const uint32_t dst = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes;
+#pragma unroll
+        for (int i = 0; i < 16 * CH; i += 32) {
+          const int at = i + lane;
+          const uint32_t o = piece<D>(at / CH, at % CH);
+          copy16(dst + o, blk + (size_t)slot * (D / 2) + at * 16);
+          copy16(dst + Group<D>::kCodes + o, blk + vofs + (size_t)slot * (D / 2) + at * 16);
+        }
+        if (lane < 8) copy16(dst + 2 * Group<D>::kCodes + lane * 16, blk + pofs + (size_t)slot * 8 + lane * 16);
+      }
+    }
+    copy_commit();
+    return there;
+  };
+  constexpr int kStride = kStep * kWarps;
+  int t0 = begin + kStep * warp;
+  uint32_t there = 0;  // two bits a stage, this step's lowest
+  look_up(t0);
+  there = issue(t0, 0);
+  look_up(t0 + kStride);
+  there |= issue(t0 + kStride, 1) << 2;
+  look_up(t0 + 2 * kStride);
+
+  // q in the order of the key words, times a power of two per row; sums of its rows
   uint32_t qf[NT][2 * KW][2];
-  float sumq[NT][2];
+  float sumq[NT][2], rowf[NT][2];
   int lim[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int row = row_first + 8 * j + r, tok = row / G;
-    float sum = 0.f;
-    if (row < rows) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + ((size_t)(q.row0 + tok) * c.heads + (size_t)h * G + (row - tok * G)) * D + t * (D / 4));
+    uint4 u[KW];
+    float sum = 0.f, big = 0.f;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint4 u = src[w];
-        qf[j][2 * w][0] = lo16(u.x, u.z);
-        qf[j][2 * w][1] = hi16(u.x, u.z);
-        qf[j][2 * w + 1][0] = lo16(u.y, u.w);
-        qf[j][2 * w + 1][1] = hi16(u.y, u.w);
-        const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+    for (int w = 0; w < KW; ++w) {
+      u[w] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        u[w] = reinterpret_cast<const uint4*>(
+            p.q + ((size_t)(q.row0 + tok) * c.heads + (size_t)h * G + (row - tok * G)) * D + t * (D / 4))[w];
+      const uint32_t e[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += __uint_as_float(e[i] << 16) + __uint_as_float(e[i] & 0xFFFF0000u);
+      for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(e[i] << 16), y = __uint_as_float(e[i] & 0xFFFF0000u);
+        sum += x + y;
+        big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
       }
-    } else {
-#pragma unroll
-      for (int w = 0; w < 2 * KW; ++w) qf[j][w][0] = qf[j][w][1] = 0u;
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const int ex = max(-100, (__float_as_int(big) >> 23) - 127);  // exponent of the largest element
+    const float fe = exp2i(14 - ex), fo = fe * 0.0625f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      // dimensions i and i + 4 of a word's eight together, as the masks leave them
+      const uint32_t e[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(e[i] << 16);
+        v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+      }
+      qf[j][2 * w][0] = pack_half2(v[0] * fe, v[4] * fe);
+      qf[j][2 * w][1] = pack_half2(v[1] * fo, v[5] * fo);
+      qf[j][2 * w + 1][0] = pack_half2(v[2] * fe, v[6] * fe);
+      qf[j][2 * w + 1][1] = pack_half2(v[3] * fo, v[7] * fo);
+    }
+    const float back = exp2i(min(127, 24 - 14 + ex)) * p.scale_log2;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4);
+      sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4) * p.scale_log2;
+      rowf[j][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
       const int rw = row_first + 8 * j + 2 * t + e;
       lim[j][e] = rw < rows ? min(end, q.len - q.n + rw / G + 1) : 0;
     }
@@ -177,63 +283,62 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) m[j][e] = -INFINITY, l[j][e] = 0.f, corr[j][e] = 0.f;
   }
-  const size_t vofs = (size_t)c.page * (D / 2), pofs = (size_t)c.page * D;
+  int ve = 1;  // exponent field of the largest value scale so far; weights carry 2^(28 - ve)
+  const int tr = (r >> 1) + 4 * (r & 1);  // the token of score row r (and of row r + 8: tr + 8)
 
-  for (int t0 = begin + kStep * warp; t0 < end; t0 += kStep * kWarps) {
+  for (int stage = 0; t0 < end; t0 += kStride) {
+    copy_wait<1>();
+    __syncwarp();
+    // the stage that the previous step has read
+    const int spare = stage == 0 ? kStages - 1 : stage - 1;
+    there |= issue(t0 + 2 * kStride, spare) << 4;
+    look_up(t0 + 3 * kStride);
+
     float sc[2][NT][4];
-    uint32_t vw[2][4][VW];
     float2 vs[2][2];
-    bool good[2];
+    unsigned vbig = 0;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int pos = t0 + 16 * g;
-      int page = -1;
-      if (pos < end) {  // the same in all lanes
-        page = kv4::page_of(c, s, pos);
-        if (page < 0 && lane == 0) kv4::report_bad();
-      }
-      good[g] = page >= 0;
-      // a group that is masked as a whole reads page 0 instead (in bounds, unused)
-      const uint8_t* blk = c.pages + kv4::block_offset(c, good[g] ? page : 0, h);
-      const int slot = pos & (c.page - 1);
-      uint32_t ka[KW], kb[KW];
-      ldg_words<KW>(ka, blk + (size_t)(slot + r) * (D / 2) + t * (D / 8));
-      ldg_words<KW>(kb, blk + (size_t)(slot + r + 8) * (D / 2) + t * (D / 8));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        ldg_words<VW>(vw[g][i], blk + vofs + (size_t)(slot + 2 * t + (i & 1) + 8 * (i >> 1)) * (D / 2) + r * (D / 16));
-      const uint2 pa = __ldg(reinterpret_cast<const uint2*>(blk + pofs + (size_t)(slot + r) * 8));
-      const uint2 pb = __ldg(reinterpret_cast<const uint2*>(blk + pofs + (size_t)(slot + r + 8) * 8));
-      vs[g][0] = half2_at(pa.y);
-      vs[g][1] = half2_at(pb.y);
+      const uint32_t kb = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes;
+      uint32_t ka[KW], kc[KW], pa[2], pb[2];
+      const uint32_t kp = D == 128 ? piece<D>(tr, t) : piece<D>(tr, t >> 1) + (t & 1) * 8;
+      lds_words<KW>(ka, kb + kp);
+      lds_words<KW>(kc, kb + kp + Group<D>::kCodes / 2);  // eight tokens on
+      lds_words<2>(pa, kb + 2 * Group<D>::kCodes + tr * 8);
+      lds_words<2>(pb, kb + 2 * Group<D>::kCodes + tr * 8 + 64);
+      vs[g][0] = half2_at(pa[1]);
+      vs[g][1] = half2_at(pb[1]);
+      const int stop = (there >> g) & 1u ? end : 0;
+      if (pos + tr < stop) vbig = max(vbig, pa[1] & 0xFFFFu);
+      if (pos + tr + 8 < stop) vbig = max(vbig, pb[1] & 0xFFFFu);
 #pragma unroll
       for (int j = 0; j < NT; ++j) sc[g][j][0] = sc[g][j][1] = sc[g][j][2] = sc[g][j][3] = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
+        const uint32_t a8 = ka[w] >> 8, c8 = kc[w] >> 8;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          mma_bf16(sc[g][j], codes<0>(ka[w]), codes<0>(kb[w]), codes<1>(ka[w]), codes<1>(kb[w]), qf[j][2 * w][0],
-                   qf[j][2 * w][1]);
-          mma_bf16(sc[g][j], codes<2>(ka[w]), codes<2>(kb[w]), codes<3>(ka[w]), codes<3>(kb[w]), qf[j][2 * w + 1][0],
-                   qf[j][2 * w + 1][1]);
+          mma_f16(sc[g][j], even4(ka[w]), even4(kc[w]), odd4(ka[w]), odd4(kc[w]), qf[j][2 * w][0], qf[j][2 * w][1]);
+          mma_f16(sc[g][j], even4(a8), even4(c8), odd4(a8), odd4(c8), qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
         }
       }
-      const float2 ks0 = half2_at(pa.x), ks1 = half2_at(pb.x);
-      const float s0 = ks0.x * p.scale_log2, b0 = fmaf(-128.f, ks0.x, ks0.y) * p.scale_log2;
-      const float s1 = ks1.x * p.scale_log2, b1 = fmaf(-128.f, ks1.x, ks1.y) * p.scale_log2;
+      const float2 k0 = half2_at(pa[0]), k1 = half2_at(pb[0]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int seen = good[g] ? lim[j][e] : 0;
-          sc[g][j][e] = pos + r < seen ? fmaf(s0, sc[g][j][e], b0 * sumq[j][e]) : -INFINITY;
-          sc[g][j][2 + e] = pos + r + 8 < seen ? fmaf(s1, sc[g][j][2 + e], b1 * sumq[j][e]) : -INFINITY;
+          const int seen = min(stop, lim[j][e]);
+          sc[g][j][e] = pos + tr < seen ? fmaf(k0.x * sc[g][j][e], rowf[j][e], k0.y * sumq[j][e]) : -INFINITY;
+          sc[g][j][2 + e] =
+              pos + tr + 8 < seen ? fmaf(k1.x * sc[g][j][2 + e], rowf[j][e], k1.y * sumq[j][e]) : -INFINITY;
         }
       }
     }
     // running maxima; the accumulators are scaled only when one has grown
+    const int ve2 = max(ve, (int)(__reduce_max_sync(0xffffffffu, vbig) >> 10));
     float ref[NT][2];
-    bool grown = false;
+    bool grown = ve2 > ve;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -246,6 +351,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
       }
     }
     if (__any_sync(0xffffffffu, grown)) {
+      const float fv = exp2i(ve - ve2);
+      ve = ve2;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float f[2];
@@ -255,6 +362,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
           m[j][e] = ref[j][e];
           l[j][e] *= f[e];
           corr[j][e] *= f[e];
+          f[e] *= fv;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -265,13 +373,15 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
         }
       }
     }
+    const float vf = exp2i(28 - ve);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       uint32_t pb[NT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int k = 0; k < 2; ++k) {
+        const float vsc = vs[g][k].x * vf;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int j = 0; j < NT; ++j) {
           float w[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -279,35 +389,41 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
             const bool in = x != -INFINITY;  // a masked place takes no part, whatever its scales hold
             const float pr = in ? ex2(x - m[j][e]) : 0.f;
             l[j][e] += pr;
-            w[e] = in ? pr * vs[g][k].x : 0.f;
+            w[e] = in ? pr * vsc : 0.f;
             if (in) corr[j][e] = fmaf(pr, vs[g][k].y, corr[j][e]);
           }
-          const __nv_bfloat162 wb = __floats2bfloat162_rn(w[0], w[1]);
-          const float2 wr = __bfloat1622float2(wb);
-          corr[j][0] = fmaf(-128.f, wr.x, corr[j][0]);
-          corr[j][1] = fmaf(-128.f, wr.y, corr[j][1]);
-          pb[j][k] = transpose8x8(*reinterpret_cast<const uint32_t*>(&wb));
+          pb[j][k] = transpose8x8(pack_half2(w[0], w[1]));
         }
       }
+      uint32_t vw[4][VW];
+      const uint32_t vb = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes + Group<D>::kCodes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        lds_words<VW>(vw[i], vb + (D == 128 ? piece<D>(t + 4 * i, r >> 1) + (r & 1) * 8
+                                            : piece<D>(t + 4 * i, r >> 2) + (r & 3) * 4));
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
-        const uint32_t a[2] = {lo16(vw[g][0][w], vw[g][1][w]), hi16(vw[g][0][w], vw[g][1][w])};
-        const uint32_t b[2] = {lo16(vw[g][2][w], vw[g][3][w]), hi16(vw[g][2][w], vw[g][3][w])};
+        const uint32_t a[2] = {lo16(vw[0][w], vw[1][w]), hi16(vw[0][w], vw[1][w])};
+        const uint32_t b[2] = {lo16(vw[2][w], vw[3][w]), hi16(vw[2][w], vw[3][w])};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const uint32_t a8 = a[i] >> 8, b8 = b[i] >> 8;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            mma_bf16(o[j][4 * w + 2 * i], codes<0>(a[i]), codes<1>(a[i]), codes<0>(b[i]), codes<1>(b[i]), pb[j][0],
-                     pb[j][1]);
-            mma_bf16(o[j][4 * w + 2 * i + 1], codes<2>(a[i]), codes<3>(a[i]), codes<2>(b[i]), codes<3>(b[i]),
-                     pb[j][0], pb[j][1]);
+            mma_f16(o[j][4 * w + 2 * i], even4(a[i]), odd4(a[i]), even4(b[i]), odd4(b[i]), pb[j][0], pb[j][1]);
+            mma_f16(o[j][4 * w + 2 * i + 1], even4(a8), odd4(a8), even4(b8), odd4(b8), pb[j][0], pb[j][1]);
           }
         }
       }
     }
+    there >>= 2;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+  copy_wait<0>();
+  __syncthreads();  // the rings become the exchange of the states
 
-  // the warps' states
+  // the warps' states: codes were c 2^-24 and c 2^-20, weights carried 2^(28 - ve)
+  const float back_even = exp2i(24 - 28 + ve), back_odd = exp2i(20 - 28 + ve);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -322,7 +438,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const Kv4AttnParams p) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         *reinterpret_cast<float2*>(&sm.o[warp][n][r * (D / 8) + 2 * i]) =
-            make_float2(o[j][i][e] + corr[j][e], o[j][i][2 + e] + corr[j][e]);
+            make_float2(fmaf(o[j][i][e], back_even, corr[j][e]), fmaf(o[j][i][2 + e], back_odd, corr[j][e]));
     }
   }
   __syncthreads();

@@ -199,7 +199,7 @@ def attention_without(b, q, scale, s, gone):
             p /= p.sum()
             v = vm[at, None] + vs[at, None] * vc[at]
             out[i, h] = p @ v
-            tol[i, h] = 2.0 ** -8 * (np.abs(out[i, h]) + p @ (vs[at, None] * vc[at])) * 1.01 + 1e-3
+            tol[i, h] = 2.0 ** -8 * np.abs(out[i, h]) + 2.0 ** -11 * (p @ (vs[at, None] * vc[at])) * 1.01 + 1e-4
     return out, tol
 
 
