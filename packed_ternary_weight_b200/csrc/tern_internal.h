@@ -351,11 +351,9 @@ int launch_kv4_read(const Kv4ReadParams& p, void* stream);
 int read_clear_dev_error_kv4(void* stream, unsigned* out);
 
 // Launch plan of the attention over few query rows: `rows` query rows per CTA
-// (8, 16 or 32), `tiles` row tiles per (sequence, kv head), positions split in
-// chunks of `chunk`, `splits` of them at the batch's largest length.
+// (8, 16 or 32) and the number of CTAs.
 struct Kv4AttnPlan {
-  int rows, tiles, chunk, splits;
-  long long units;            // (sequence, kv head, row tile)
+  int rows, ctas;
   size_t cnt_bytes, ws_bytes;
 };
 struct Kv4AttnParams {
@@ -364,9 +362,8 @@ struct Kv4AttnParams {
   uint16_t* out;
   float scale_log2;           // scale * log2(e)
   int group;                  // query heads per kv head
-  int tiles, chunk, splits;
-  unsigned* cnt;              // [units], zero on entry and exit
-  float* part;                // [units][splits][rows][dim + 2]
+  unsigned* cnt;              // [CTAs], zero on entry and exit
+  float* part;                // [CTAs][2][rows * (dim + 2)]
 };
 int launch_kv4_attn(const Kv4AttnParams& p, const Kv4AttnPlan& plan, void* stream);
 int read_clear_dev_error_kv4_attn(void* stream, unsigned* out);

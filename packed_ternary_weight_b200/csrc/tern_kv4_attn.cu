@@ -36,10 +36,15 @@
 // hold 139 KB in flight. The stage is swizzled in 16-byte pieces so that both
 // products read it without bank conflicts.
 //
-// Split. A CTA takes (sequence, kv head, tile of query rows, chunk of
-// positions); its eight warps take 32 positions in turn with softmax states of
-// their own, joined in shared memory. Chunks of one tile are joined by the last
-// CTA to arrive, in chunk order, so results do not depend on timing.
+// Split. The work is one line of rounds, 256 positions of a (sequence, kv head,
+// tile of query rows), laid end to end over the whole batch; CTA c of G takes
+// the rounds [W c / G, W (c + 1) / G), so every CTA reads the same number of
+// positions whatever the lengths are, in one resident wave. Inside a CTA the
+// eight warps take 32 positions in turn with softmax states of their own, joined
+// in shared memory. A tile that CTA boundaries cut is joined by the last of its
+// CTAs to arrive, in position order, so results do not depend on timing. A CTA
+// holds at most one tile that it begins and does not end and one that it ends
+// or passes through, so two slots of the workspace per CTA are enough.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -59,6 +64,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;   // positions a warp takes at a time
 constexpr int kStages = 3;  // of its ring
+constexpr int kRound = kStep * kWarps;  // positions of a CTA's round
+constexpr int kMaxCtas = 512;           // of a launch
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -130,22 +137,34 @@ struct Shared {
       float m[kWarps][kRows], l[kWarps][kRows];
       float o[kWarps][kRows][kPitch];
     };
+    struct {
+      float sum[kRows];                    // of a join: the rows' sums,
+      float2 ml[kMaxCtas][kRows];          // maxima and sums of the parts, then (factor, -)
+    };
   };
+  long long scan[kWarps + 1];              // the search for the CTA's first round
+  long long found_off;
+  int found;
   int last;
 };
 
-// Joins `n` softmax states (m_i, l_i, o_i[4]) in order; the factor of each is 2^(m_i - max).
-struct Join {
-  float mx = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  __device__ __forceinline__ void add(float m, float li, float4 v) {
-    const float w = m == -INFINITY ? 0.f : ex2(m - mx);
-    l = fmaf(w, li, l);
-    o[0] = fmaf(w, v.x, o[0]);
-    o[1] = fmaf(w, v.y, o[1]);
-    o[2] = fmaf(w, v.z, o[2]);
-    o[3] = fmaf(w, v.w, o[3]);
-  }
-};
+// Rounds of a sequence: kv heads x row tiles x rounds of its positions.
+__device__ __forceinline__ long long rounds_of(const Kv4AttnParams& p, const kv4::Seq& q, int R, int* tiles,
+                                               int* rounds) {
+  *tiles = (q.n * p.group + R - 1) / R;
+  *rounds = max(1, (q.len + kRound - 1) / kRound);
+  return q.ok ? (long long)p.c.kv_heads * *tiles * *rounds : 0;
+}
+
+__device__ __forceinline__ void store_row(const Kv4AttnParams& p, const kv4::Seq& q, int D, int h, int row, int d,
+                                          const float (&o)[4], float l) {
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);  // no position: zero; NaN stays
+  const int tok = row / p.group;
+  __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o[0] * inv, o[1] * inv), __floats2bfloat162_rn(o[2] * inv, o[3] * inv)};
+  *reinterpret_cast<uint2*>(
+      p.out + ((size_t)(q.row0 + tok) * p.c.heads + (size_t)h * p.group + (row - tok * p.group)) * D + d) =
+      *reinterpret_cast<const uint2*>(v);
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const Kv4AttnParams p) {
@@ -158,22 +177,92 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
   Shared<D, NT>& sm = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
   const Kv4Params& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-  const int unit = blockIdx.x / p.splits, sp = blockIdx.x - unit * p.splits;
-  const int tile = unit % p.tiles, sh = unit / p.tiles;
-  const int h = sh % c.kv_heads, s = sh / c.kv_heads;
-  const kv4::Seq q = kv4::load_seq(c, s);
-  if (!q.ok) {
-    if (sp == 0 && threadIdx.x == 0) kv4::report_bad();
-    return;
+  const int G = p.group;
+  const size_t vofs = (size_t)c.page * (D / 2), pofs = (size_t)c.page * D;
+  const uint32_t ring = smem_u32(sm.ring[warp]);
+
+  // this CTA's rounds [at, stop_at) and the sequence and place of the first
+  long long total, ctas, at, stop_at;
+  int s = 0;
+  long long in_seq;  // rounds of sequence s before `at`
+  {
+    int tiles, rounds;
+    auto weight = [&](int i, bool report) -> long long {
+      const kv4::Seq q = kv4::load_seq(c, i);
+      if (!q.ok && report) kv4::report_bad();
+      return rounds_of(p, q, R, &tiles, &rounds);
+    };
+    auto block_sum = [&](long long v) {
+#pragma unroll
+      for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+      if (lane == 0) sm.scan[warp] = v;
+      __syncthreads();
+      long long all = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) all += sm.scan[i];
+      __syncthreads();
+      return all;
+    };
+    if (c.seqs == 1) {
+      total = weight(0, blockIdx.x == 0 && threadIdx.x == 0);
+    } else {
+      long long mine = 0;
+      for (int i = threadIdx.x; i < c.seqs; i += kThreads) mine += weight(i, blockIdx.x == 0);
+      total = block_sum(mine);
+    }
+    ctas = min((long long)gridDim.x, total);  // each of them holds a round
+    if (blockIdx.x >= ctas) return;
+    at = total * blockIdx.x / ctas;
+    stop_at = total * (blockIdx.x + 1) / ctas;
+    in_seq = at;
+    if (c.seqs > 1) {
+      long long before = 0;
+      for (int base = 0; base < c.seqs; base += kThreads) {
+        const int i = base + threadIdx.x;
+        const long long w = i < c.seqs ? weight(i, false) : 0;
+        long long incl = w;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, k);
+          if (lane >= k) incl += v;
+        }
+        if (lane == 31) sm.scan[warp] = incl;
+        if (threadIdx.x == 0) sm.found = -1;
+        __syncthreads();
+        long long pre = before;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          if (k < warp) pre += sm.scan[k];
+          before += sm.scan[k];
+        }
+        if (at >= pre + incl - w && at < pre + incl) {
+          sm.found = i;
+          sm.found_off = at - (pre + incl - w);
+        }
+        __syncthreads();
+        if (sm.found >= 0) break;
+      }
+      s = sm.found;
+      in_seq = sm.found_off;
+      if (s < 0) return;  // the lengths changed meanwhile
+    }
   }
-  const int G = p.group, rows = q.n * G, row_first = tile * R;
-  if (row_first >= rows) return;
+
+  for (; at < stop_at && s < c.seqs; ++s, in_seq = 0) {  // sequences
+  const kv4::Seq q = kv4::load_seq(c, s);
+  int tiles, rounds;
+  const long long seq_rounds = rounds_of(p, q, R, &tiles, &rounds);
+  const int rows = q.n * G;
+  while (in_seq < seq_rounds && at < stop_at) {  // the (kv head, tile) ranges of one sequence
+  const int unit = (int)(in_seq / rounds), round0 = (int)(in_seq - (long long)unit * rounds);
+  const int take = (int)min((long long)(rounds - round0), stop_at - at);
+  const long long unit_first = at - round0;  // the unit's first round among all
+  at += take;
+  in_seq += take;
+  const int h = unit / tiles, tile = unit - h * tiles, row_first = tile * R;
   const int row_last = min(rows, row_first + R) - 1;
   const int limit_max = q.len - q.n + row_last / G + 1;  // positions that the tile's last token sees
-  const int ns = limit_max > 0 ? (limit_max + p.chunk - 1) / p.chunk : 1;
-  if (sp >= ns) return;
-  const int begin = sp * p.chunk, end = min(limit_max, begin + p.chunk);
-  const size_t vofs = (size_t)c.page * (D / 2), pofs = (size_t)c.page * D;
+  const int begin = round0 * kRound, end = (int)min((long long)limit_max, (long long)(round0 + take) * kRound);
 
   // the warp's steps: pages are looked up one step before their copies are issued
   int pg[2];
@@ -188,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
       }
     }
   };
-  const uint32_t ring = smem_u32(sm.ring[warp]);
   // copies of the step at t0 into a stage; returns which of its groups are there
   auto issue = [&](int t0, int stage) {
     uint32_t there = 0;
@@ -442,103 +530,116 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
     }
   }
   __syncthreads();
-  float* part = p.part + ((size_t)unit * p.splits + sp) * (R * (D + 2));
+  // the tile's CTAs: the first holds its first round, the last its last
+  const int first_cta = (int)(((unit_first + 1) * ctas - 1) / total);
+  const int last_cta = (int)(((unit_first + rounds) * ctas - 1) / total);
+  const bool whole = first_cta == last_cta;
+  constexpr int kSlot = R * (D + 2);  // floats: weighted values [R][D], then (maximum, sum) [R]
+  float* part = p.part + (size_t)(2 * blockIdx.x + (round0 == 0 ? 1 : 0)) * kSlot;
   for (int item = threadIdx.x; item < R * (D / 4); item += kThreads) {
     const int n = item / (D / 4), d = (item - n * (D / 4)) * 4;
-    const int row = row_first + n;
-    if (row >= rows) continue;
-    Join a;
+    if (row_first + n >= rows) continue;
+    float mx = -INFINITY, sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) a.mx = fmaxf(a.mx, sm.m[w][n]);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][n]);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) a.add(sm.m[w][n], sm.l[w][n], *reinterpret_cast<const float4*>(&sm.o[w][n][d]));
-    if (ns == 1) {
-      const float inv = a.l > 0.f ? 1.0f / a.l : (a.l == 0.f ? 0.f : a.l);  // no position: zero; NaN stays
-      const int tok = row / G;
-      __nv_bfloat162 v[2] = {__floats2bfloat162_rn(a.o[0] * inv, a.o[1] * inv),
-                             __floats2bfloat162_rn(a.o[2] * inv, a.o[3] * inv)};
-      *reinterpret_cast<uint2*>(p.out + ((size_t)(q.row0 + tok) * c.heads + (size_t)h * G + (row - tok * G)) * D + d) =
-          *reinterpret_cast<const uint2*>(v);
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sm.m[w][n] == -INFINITY ? 0.f : ex2(sm.m[w][n] - mx);
+      const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][n][d]);
+      sum = fmaf(f, sm.l[w][n], sum);
+      v[0] = fmaf(f, x.x, v[0]);
+      v[1] = fmaf(f, x.y, v[1]);
+      v[2] = fmaf(f, x.z, v[2]);
+      v[3] = fmaf(f, x.w, v[3]);
+    }
+    if (whole) {
+      store_row(p, q, D, h, row_first + n, d, v, sum);
     } else {
-      float* dst = part + (size_t)n * (D + 2);
-      *reinterpret_cast<float2*>(dst + d) = make_float2(a.o[0], a.o[1]);
-      *reinterpret_cast<float2*>(dst + d + 2) = make_float2(a.o[2], a.o[3]);
-      if (d == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(a.mx, a.l);
+      *reinterpret_cast<float4*>(part + n * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+      if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * n) = make_float2(mx, sum);
     }
   }
-  if (ns == 1) return;
-
-  // the last chunk of the tile to arrive joins all of them
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    sm.last = atomicAdd(p.cnt + unit, 1u) == (unsigned)(ns - 1);
-    if (sm.last) p.cnt[unit] = 0u;
-  }
-  __syncthreads();
-  if (!sm.last) return;
-  __threadfence();
-  const float* first = p.part + (size_t)unit * p.splits * (R * (D + 2));
-  for (int item = threadIdx.x; item < R * (D / 4); item += kThreads) {
-    const int n = item / (D / 4), d = (item - n * (D / 4)) * 4;
-    const int row = row_first + n;
-    if (row >= rows) continue;
-    const float* src = first + (size_t)n * (D + 2);
-    Join a;
-    for (int i = 0; i < ns; ++i) a.mx = fmaxf(a.mx, __ldcg(src + (size_t)i * (R * (D + 2)) + D));
-    for (int i = 0; i < ns; ++i) {
-      const float* e = src + (size_t)i * (R * (D + 2));
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(e + D));
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(e + d)), y = __ldcg(reinterpret_cast<const float2*>(e + d + 2));
-      a.add(ml.x, ml.y, make_float4(x.x, x.y, y.x, y.y));
+  if (!whole) {
+    // the last CTA of the tile to arrive joins its parts
+    const int ns = last_cta - first_cta + 1;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sm.last = atomicAdd(p.cnt + first_cta, 1u) == (unsigned)(ns - 1);
+      if (sm.last) p.cnt[first_cta] = 0u;
     }
-    const float inv = a.l > 0.f ? 1.0f / a.l : (a.l == 0.f ? 0.f : a.l);
-    const int tok = row / G;
-    __nv_bfloat162 v[2] = {__floats2bfloat162_rn(a.o[0] * inv, a.o[1] * inv),
-                           __floats2bfloat162_rn(a.o[2] * inv, a.o[3] * inv)};
-    *reinterpret_cast<uint2*>(p.out + ((size_t)(q.row0 + tok) * c.heads + (size_t)h * G + (row - tok * G)) * D + d) =
-        *reinterpret_cast<const uint2*>(v);
+    __syncthreads();
+    if (sm.last) {
+      __threadfence();
+      const float* parts = p.part + (size_t)2 * first_cta * kSlot;
+      auto slot = [&](int i) { return parts + (size_t)(i == 0 ? 1 : 2 * i) * kSlot; };
+      for (int i = threadIdx.x; i < ns * R; i += kThreads)
+        sm.ml[i / R][i % R] = __ldcg(reinterpret_cast<const float2*>(slot(i / R) + R * D + 2 * (i % R)));
+      __syncthreads();
+      for (int n = warp; n < R; n += kWarps) {  // a warp per row: every part's factor, and the sum
+        if (row_first + n >= rows) continue;    // unwritten
+        float mx = -INFINITY, sum = 0.f;
+        for (int i = lane; i < ns; i += 32) mx = fmaxf(mx, sm.ml[i][n].x);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+        for (int i = lane; i < ns; i += 32) {
+          const float2 e = sm.ml[i][n];
+          const float f = e.x == -INFINITY ? 0.f : ex2(e.x - mx);
+          sum = fmaf(f, e.y, sum);
+          sm.ml[i][n].x = f;
+        }
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane == 0) sm.sum[n] = sum;
+      }
+      __syncthreads();
+      for (int item = threadIdx.x; item < R * (D / 4); item += kThreads) {
+        const int n = item / (D / 4), d = (item - n * (D / 4)) * 4;
+        if (row_first + n >= rows) continue;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = 0; i < ns; ++i) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i) + n * D + d));
+          const float f = sm.ml[i][n].x;
+          v[0] = fmaf(f, x.x, v[0]);
+          v[1] = fmaf(f, x.y, v[1]);
+          v[2] = fmaf(f, x.z, v[2]);
+          v[3] = fmaf(f, x.w, v[3]);
+        }
+        store_row(p, q, D, h, row_first + n, d, v, sm.sum[n]);
+      }
+    }
+  }
+  __syncthreads();  // the exchange becomes the rings again
+  }
   }
 }
 
 template <int D, int NT>
-int launch_one(const Kv4AttnParams& p, long long blocks, cudaStream_t s) {
+int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
   constexpr int bytes = (int)sizeof(Shared<D, NT>);
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return (int)e;
-  attn_kernel<D, NT><<<(unsigned)blocks, kThreads, bytes, s>>>(p);
+  attn_kernel<D, NT><<<ctas, kThreads, bytes, s>>>(p);
   return (int)cudaGetLastError();
 }
 
 // Rows per CTA: the smallest of 8, 16, 32 that holds a sequence's rows of one
-// kv head, else tiles of 32. Chunks: enough CTAs for about eight per
-// multiprocessor at the batch's largest length, whole rounds of the eight warps.
-constexpr int kRound = kStep * kWarps;
-long long target_ctas(int sms) { return 8ll * sms; }
-// A batch is split only while it has fewer tiles than the target, so the
-// counters, one per tile, have a place whose size no batch changes.
-size_t counter_bytes(int sms) { return ((size_t)target_ctas(sms) * 4 + 255) / 256 * 256; }
-
+// kv head, else tiles of 32. One resident wave: two CTAs per multiprocessor
+// with 8 rows, one with more (registers), and no more CTAs than rounds.
 tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int max_len, int sms, Kv4AttnPlan* pl) {
   const long long rows = (long long)max_new * (heads / c.kv_heads);
   if (rows > (1 << 30)) return TERN_EUNSUPPORTED;
   pl->rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-  const long long tiles = (rows + pl->rows - 1) / pl->rows;
-  pl->tiles = (int)tiles;
-  pl->units = (long long)seqs * c.kv_heads * tiles;
-  const long long target = target_ctas(sms);
-  long long splits = pl->units > 0 ? (target + pl->units - 1) / pl->units : 1;
-  splits = std::max(1ll, std::min(splits, ((long long)max_len + kRound - 1) / kRound));
-  long long chunk = (max_len + splits - 1) / splits;
-  chunk = std::max((long long)kRound, (chunk + kRound - 1) / kRound * kRound);
-  pl->chunk = (int)std::min(chunk, 1ll << 30);
-  pl->splits = std::max(1, (int)(((long long)max_len + pl->chunk - 1) / pl->chunk));
-  if (pl->units * pl->splits > 0x7FFFFFFFll) return TERN_EUNSUPPORTED;
-  pl->cnt_bytes = counter_bytes(sms);
-  pl->ws_bytes = pl->splits > 1
-                     ? pl->cnt_bytes + (size_t)pl->units * pl->splits * pl->rows * (size_t)(c.dim + 2) * 4
-                     : 0;
+  const long long tiles = (rows + pl->rows - 1) / pl->rows, rounds = std::max(1, (max_len - 1) / kRound + 1);
+  // seqs x kv_heads x tiles x rounds must stay below 2^63 / kMaxCtas in the kernel
+  const double most = (double)seqs * c.kv_heads * (double)tiles * (double)rounds;
+  if (most > 1e15) return TERN_EUNSUPPORTED;
+  const int wave = std::min(kMaxCtas, (pl->rows == 8 ? 2 : 1) * sms);
+  pl->ctas = (int)std::min((double)wave, std::max(1.0, most));
+  // two slots per CTA of the largest wave, and a counter, at places that no batch changes
+  pl->cnt_bytes = kMaxCtas * sizeof(unsigned);
+  pl->ws_bytes = rounds > 1 ? pl->cnt_bytes + (size_t)wave * 2 * pl->rows * (size_t)(c.dim + 2) * 4 : 0;
   return TERN_OK;
 }
 
@@ -546,7 +647,7 @@ tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int 
 
 int launch_kv4_attn(const Kv4AttnParams& p, const Kv4AttnPlan& pl, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long blocks = pl.units * pl.splits;
+  const int blocks = pl.ctas;
   if (p.c.dim == 128) {
     if (pl.rows == 8) return launch_one<128, 1>(p, blocks, s);
     if (pl.rows == 16) return launch_one<128, 2>(p, blocks, s);
@@ -569,15 +670,10 @@ extern "C" tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* c
   if (st != TERN_OK) return st;
   if (seqs < 0 || seqs > 65535 || max_new < 0 || max_len < 0 || heads < 1 || heads % c.kv_heads != 0)
     return TERN_EINVAL;
-  const int sms = sm_count();
   Kv4AttnPlan pl{};
-  const tern_status sp = plan_attn(c, heads, seqs, max_new, max_len, sms, &pl);
+  const tern_status sp = plan_attn(c, heads, seqs, max_new, max_len, sm_count(), &pl);
   if (sp != TERN_OK) return sp;
-  // tiles x chunks of any batch within the bounds that is split at all: fewer
-  // tiles than the target, and one chunk more per tile than divides it
-  *bytes = seqs > 0 && max_new > 0 && max_len > kRound
-               ? pl.cnt_bytes + 2 * (size_t)target_ctas(sms) * pl.rows * (size_t)(c.dim + 2) * 4
-               : 0;
+  *bytes = seqs > 0 && max_new > 0 ? pl.ws_bytes : 0;
   return TERN_OK;
 }
 
@@ -604,9 +700,6 @@ extern "C" tern_status tern_kv4_attention(const tern_kv4_cache* cache, const ter
   p.out = d_out;
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.group = heads / p.c.kv_heads;
-  p.tiles = pl.tiles;
-  p.chunk = pl.chunk;
-  p.splits = pl.splits;
   p.cnt = static_cast<unsigned*>(d_ws);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + pl.cnt_bytes);
   return launch_kv4_attn(p, pl, stream) == 0 ? TERN_OK : TERN_ECUDA;
