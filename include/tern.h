@@ -484,7 +484,8 @@ tern_status tern_kv4_read(const tern_kv4_cache* cache, const tern_kv4_batch* bat
 
 /* Workspace of tern_kv4_attention for batches of up to `seqs` sequences, max_new
  * new tokens and max_len positions each: 256-byte aligned, zero-filled before
- * its first use and left ready for the next call. Calls that may run at the same
+ * its first use and left ready for the next call (a call that reported
+ * TERN_ETIMEOUT excepted: zero-fill it again). Calls that may run at the same
  * time need separate workspaces. */
 tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32_t seqs, int32_t max_new,
                                               int32_t max_len, int32_t heads, size_t* bytes);

@@ -28,13 +28,17 @@
 // transposed too, dimensions x rows: its A operand pairs the same dimension of
 // two tokens by byte permutation, and its B operand is the probability matrix
 // transposed in registers by movmatrix. Row x of a score block stands for token
-// (x >> 1) + 4 (x & 1), which puts the tokens that four lanes read together in
-// the second product next to one another.
+// x ^ (x >> 1 & 1): four lanes then read two even and two odd tokens together
+// in the second product, whose shared-memory reads meet in two instead of four
+// ways, and the first product's reads stay free of conflicts.
 //
-// Memory. Each warp has a ring of its own of three stages of 32 tokens, filled
-// by 16-byte asynchronous copies two stages ahead; 16 warps per multiprocessor
-// hold 139 KB in flight. The stage is swizzled in 16-byte pieces so that both
-// products read it without bank conflicts.
+// Memory. A page's block of one head is contiguous, so a round of 256 positions
+// arrives in 256 / page_size bulk copies, into a ring of three stages of a round
+// each; two CTAs per multiprocessor keep 139 KB in flight. The warp that requests a
+// round changes with every round. The kernel is bound by its bit operations
+// (masks, shifts and byte permutations run at half the issue rate: about 90 of
+// them per lane and 16 tokens), so rounds that every row sees as a whole take a
+// path without masks.
 //
 // Split. The work is one line of rounds, 256 positions of a (sequence, kv head,
 // tile of query rows), laid end to end over the whole batch; CTA c of G takes
@@ -50,9 +54,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "tern_kv4.cuh"
+#include "tern_tc.cuh"
 
 namespace tern {
 
@@ -63,7 +69,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;   // positions a warp takes at a time
-constexpr int kStages = 3;  // of its ring
+constexpr int kStages = 3;  // rounds in the ring
 constexpr int kRound = kStep * kWarps;  // positions of a CTA's round
 constexpr int kMaxCtas = 512;           // of a launch
 
@@ -97,27 +103,6 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Where piece `c` (16 bytes) of token j's codes stands within a group of 16 tokens.
-template <int D>
-__device__ __forceinline__ uint32_t piece(int j, int c) {
-  if constexpr (D == 128) return (uint32_t)((j >> 1) * 128 + (((((j & 1) << 2) | c) ^ (j & 6)) << 4));
-  return (uint32_t)((j >> 2) * 128 + (((((j & 3) << 1) | c) ^ (j & 4)) << 4));
-}
-template <int D>
-struct Group {
-  static constexpr int kCodes = 16 * D / 2;           // bytes of 16 tokens' codes (keys or values)
-  static constexpr int kBytes = 2 * kCodes + 16 * 8;  // and their scale pairs
-};
-
 template <int WORDS>
 __device__ __forceinline__ void lds_words(uint32_t (&v)[WORDS], uint32_t a) {
   if constexpr (WORDS == 4)
@@ -132,7 +117,7 @@ template <int D, int NT>
 struct Shared {
   static constexpr int kRows = 8 * NT, kPitch = D + 4;
   union {
-    uint8_t ring[kWarps][kStages][2 * Group<D>::kBytes];
+    uint8_t ring[kStages][kRound * (D + 8)];
     struct {
       float m[kWarps][kRows], l[kWarps][kRows];
       float o[kWarps][kRows][kPitch];
@@ -142,6 +127,10 @@ struct Shared {
       float2 ml[kMaxCtas][kRows];          // maxima and sums of the parts, then (factor, -)
     };
   };
+  uint64_t full[kStages], empty[kStages];
+  uint32_t there[kStages];                 // pages of a stage that are in the cache, one bit each
+  uint32_t phase[kStages];                 // of a stage's last request; 2: none yet
+  uint32_t abort;                          // a bounded wait has given up
   long long scan[kWarps + 1];              // the search for the CTA's first round
   long long found_off;
   int found;
@@ -166,20 +155,188 @@ __device__ __forceinline__ void store_row(const Kv4AttnParams& p, const kv4::Seq
       *reinterpret_cast<const uint2*>(v);
 }
 
+// A warp's softmax state and queries: NT tiles of eight rows; the lane holds
+// rows 2t, 2t + 1 of each and, of the output, dimensions r D/8 .. + D/8 - 1.
+template <int D, int NT>
+struct State {
+  uint32_t qf[NT][D / 16][2];
+  float sumq[NT][2], rowf[NT][2];
+  int lim[NT][2];  // positions that a row sees
+  float o[NT][D / 16][4], m[NT][2], l[NT][2], corr[NT][2];
+  int ve;          // exponent field of the largest value scale so far; weights carry 2^(28 - ve)
+};
+
+// 32 positions from pos0 on. kb, pb: shared addresses of the keys' codes and
+// of the scale pairs of each group of 16, already moved to the lane's place;
+// the values' codes at vb. FULL: every row sees all of them; otherwise
+// positions from stop[g] on are masked.
+template <int D, int NT, bool FULL>
+__device__ __forceinline__ void step(State<D, NT>& S, int pos0, const uint32_t (&kb)[2], const uint32_t (&vb)[2],
+                                     const uint32_t (&pb)[2], const int (&stop)[2], int tr, int tx) {
+  constexpr int KW = D / 32, VW = D / 64, MT = D / 16;
+  float sc[2][NT][4];
+  float2 vs[2][2];
+  unsigned vbig = 0;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int pos = pos0 + 16 * g;
+    uint32_t ka[KW], kc[KW], pa[2], pc[2];
+    lds_words<KW>(ka, kb[g]);
+    lds_words<KW>(kc, kb[g] + 8 * (D / 2));
+    lds_words<2>(pa, pb[g]);
+    lds_words<2>(pc, pb[g] + 64);
+    vs[g][0] = half2_at(pa[1]);
+    vs[g][1] = half2_at(pc[1]);
+    if (FULL || pos + tr < stop[g]) vbig = max(vbig, pa[1] & 0xFFFFu);
+    if (FULL || pos + tr + 8 < stop[g]) vbig = max(vbig, pc[1] & 0xFFFFu);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sc[g][j][0] = sc[g][j][1] = sc[g][j][2] = sc[g][j][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const uint32_t a8 = ka[w] >> 8, c8 = kc[w] >> 8;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        mma_f16(sc[g][j], even4(ka[w]), even4(kc[w]), odd4(ka[w]), odd4(kc[w]), S.qf[j][2 * w][0], S.qf[j][2 * w][1]);
+        mma_f16(sc[g][j], even4(a8), even4(c8), odd4(a8), odd4(c8), S.qf[j][2 * w + 1][0], S.qf[j][2 * w + 1][1]);
+      }
+    }
+    const float2 k0 = half2_at(pa[0]), k1 = half2_at(pc[0]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = fmaf(k0.x * sc[g][j][e], S.rowf[j][e], k0.y * S.sumq[j][e]);
+        const float y = fmaf(k1.x * sc[g][j][2 + e], S.rowf[j][e], k1.y * S.sumq[j][e]);
+        const int seen = FULL ? 0 : min(stop[g], S.lim[j][e]);
+        sc[g][j][e] = FULL || pos + tr < seen ? x : -INFINITY;
+        sc[g][j][2 + e] = FULL || pos + tr + 8 < seen ? y : -INFINITY;
+      }
+    }
+  }
+  // running maxima; the accumulators are scaled only when one has grown
+  const int ve2 = max(S.ve, (int)(__reduce_max_sync(0xffffffffu, vbig) >> 10));
+  float ref[NT][2];
+  bool grown = ve2 > S.ve;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = fmaxf(fmaxf(sc[0][j][e], sc[0][j][2 + e]), fmaxf(sc[1][j][e], sc[1][j][2 + e]));
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+      grown |= x > S.m[j][e];
+      ref[j][e] = fmaxf(x, S.m[j][e]);
+    }
+  }
+  if (__any_sync(0xffffffffu, grown)) {
+    const float fv = exp2i(S.ve - ve2);
+    S.ve = ve2;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[e] = S.m[j][e] == -INFINITY ? 0.f : ex2(S.m[j][e] - ref[j][e]);
+        S.m[j][e] = ref[j][e];
+        S.l[j][e] *= f[e];
+        S.corr[j][e] *= f[e];
+        f[e] *= fv;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        S.o[j][i][0] *= f[0];
+        S.o[j][i][1] *= f[1];
+        S.o[j][i][2] *= f[0];
+        S.o[j][i][3] *= f[1];
+      }
+    }
+  }
+  const float vf = exp2i(28 - S.ve);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t pw[NT][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float vsc = vs[g][k].x * vf;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = sc[g][j][2 * k + e];
+          const bool in = FULL || x != -INFINITY;  // a masked place takes no part, whatever its scales hold
+          const float pr = in ? ex2(x - S.m[j][e]) : 0.f;
+          S.l[j][e] += pr;
+          w[e] = in ? pr * vsc : 0.f;
+          if (in) S.corr[j][e] = fmaf(pr, vs[g][k].y, S.corr[j][e]);
+        }
+        pw[j][k] = transpose8x8(pack_half2(w[0], w[1]));
+      }
+    }
+    // the lane's tokens of the second product: rows 2t and 2t + 1, and eight on
+    uint32_t va[VW], vc[VW], vd[VW], ve[VW];
+    const uint32_t first = vb[g] + (tx ? D / 2 : 0), second = vb[g] + (tx ? 0 : D / 2);
+    lds_words<VW>(va, first);
+    lds_words<VW>(vc, second);
+    lds_words<VW>(vd, first + 8 * (D / 2));
+    lds_words<VW>(ve, second + 8 * (D / 2));
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const uint32_t a[2] = {lo16(va[w], vc[w]), hi16(va[w], vc[w])};
+      const uint32_t b[2] = {lo16(vd[w], ve[w]), hi16(vd[w], ve[w])};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t a8 = a[i] >> 8, b8 = b[i] >> 8;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_f16(S.o[j][4 * w + 2 * i], even4(a[i]), odd4(a[i]), even4(b[i]), odd4(b[i]), pw[j][0], pw[j][1]);
+          mma_f16(S.o[j][4 * w + 2 * i + 1], even4(a8), odd4(a8), even4(b8), odd4(b8), pw[j][0], pw[j][1]);
+        }
+      }
+    }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const Kv4AttnParams p) {
   constexpr int R = 8 * NT;          // query rows of the tile
   constexpr int KW = D / 32;         // words of K codes per lane and token
-  constexpr int VW = D / 64;         // words of V codes per lane and token
   constexpr int MT = D / 16;         // 16-dimension tiles of the output
-  constexpr int CH = D / 32;         // 16-byte pieces of a token's codes
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Shared<D, NT>& sm = *reinterpret_cast<Shared<D, NT>*>(smem_raw);
   const Kv4Params& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   const int G = p.group;
-  const size_t vofs = (size_t)c.page * (D / 2), pofs = (size_t)c.page * D;
-  const uint32_t ring = smem_u32(sm.ring[warp]);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kWarps);
+      sm.phase[i] = 2;
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  volatile uint32_t* abort = &sm.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!*abort && !mbar_wait_bounded(bar, parity)) *abort = 1;
+  };
+
+  // where the warp's two groups of 16 tokens stand in a stage: their page's
+  // block, then keys, values and scale pairs at the lane's token and dimensions
+  const int tr = r ^ ((r >> 1) & 1), tx = t & 1;
+  const uint32_t block_bytes = (uint32_t)c.page * (D + 8);
+  uint32_t okb[2], ovb[2], opb[2];
+  int page_bit[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int tau = kStep * warp + 16 * g, slot = tau & (c.page - 1);
+    page_bit[g] = tau >> c.log_page;
+    const uint32_t blk = smem_u32(sm.ring) + (uint32_t)page_bit[g] * block_bytes;
+    okb[g] = blk + (uint32_t)(slot + tr) * (D / 2) + t * (D / 8);
+    ovb[g] = blk + (uint32_t)(c.page + slot + 2 * t) * (D / 2) + r * (D / 16);
+    opb[g] = blk + (uint32_t)c.page * D + (uint32_t)(slot + tr) * 8;
+  }
 
   // this CTA's rounds [at, stop_at) and the sequence and place of the first
   long long total, ctas, at, stop_at;
@@ -248,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
     }
   }
 
+  const uint64_t policy = policy_evict_first();
+  int use = 0;  // rounds this CTA has taken
   for (; at < stop_at && s < c.seqs; ++s, in_seq = 0) {  // sequences
   const kv4::Seq q = kv4::load_seq(c, s);
   int tiles, rounds;
@@ -264,55 +423,38 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
   const int limit_max = q.len - q.n + row_last / G + 1;  // positions that the tile's last token sees
   const int begin = round0 * kRound, end = (int)min((long long)limit_max, (long long)(round0 + take) * kRound);
 
-  // the warp's steps: pages are looked up one step before their copies are issued
-  int pg[2];
-  auto look_up = [&](int t0) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int pos = t0 + 16 * g;
-      pg[g] = -1;
-      if (pos < end) {  // the same in all lanes
-        pg[g] = kv4::page_of(c, s, pos);
-        if (pg[g] < 0 && lane == 0) kv4::report_bad();
-      }
-    }
+  // Rounds of this range arrive in the ring in turn; round number `use` counts
+  // over the CTA's whole life. The pages of a round are looked up by one warp,
+  // a lane a page, and requested when the stage's last round has been read.
+  const int n_rounds = end > begin ? (end - begin + kRound - 1) / kRound : 0;
+  auto look_up = [&](int i) {  // page of this lane in the range's round i; -1: not there, -2: beyond the end
+    const int pos = begin + i * kRound + (lane << c.log_page);
+    if ((lane << c.log_page) >= kRound || pos >= end) return -2;
+    const int page = kv4::page_of(c, s, pos);
+    if (page < 0) kv4::report_bad();
+    return page;
   };
-  // copies of the step at t0 into a stage; returns which of its groups are there
-  auto issue = [&](int t0, int stage) {
-    uint32_t there = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (pg[g] >= 0) {
-        there |= 1u << g;
-        const int slot = (t0 + 16 * g) & (c.page - 1);
-        const uint8_t* blk = c.pages + kv4::block_offset(c, pg[g], h);
-        const uint32_t dst = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes;
-#pragma unroll
-        for (int i = 0; i < 16 * CH; i += 32) {
-          const int at = i + lane;
-          const uint32_t o = piece<D>(at / CH, at % CH);
-          copy16(dst + o, blk + (size_t)slot * (D / 2) + at * 16);
-          copy16(dst + Group<D>::kCodes + o, blk + vofs + (size_t)slot * (D / 2) + at * 16);
-        }
-        if (lane < 8) copy16(dst + 2 * Group<D>::kCodes + lane * 16, blk + pofs + (size_t)slot * 8 + lane * 16);
-      }
+  auto request = [&](int page, int n) {  // the CTA's round number n
+    const int stage = n % kStages;
+    if (n >= kStages) wait(&sm.empty[stage], (uint32_t)(n / kStages - 1) & 1u);
+    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+    if (*abort) return;
+    if (lane == 0) {
+      sm.there[stage] = there;
+      sm.phase[stage] = (uint32_t)(n / kStages) & 1u;
+      mbar_arrive_expect_tx(&sm.full[stage], (uint32_t)__popc(there) * block_bytes);
     }
-    copy_commit();
-    return there;
+    __syncwarp();
+    if (page >= 0)
+      bulk_g2s(sm.ring[stage] + (uint32_t)lane * block_bytes, c.pages + kv4::block_offset(c, page, h), block_bytes,
+               &sm.full[stage], policy);
   };
-  constexpr int kStride = kStep * kWarps;
-  int t0 = begin + kStep * warp;
-  uint32_t there = 0;  // two bits a stage, this step's lowest
-  look_up(t0);
-  there = issue(t0, 0);
-  look_up(t0 + kStride);
-  there |= issue(t0 + kStride, 1) << 2;
-  look_up(t0 + 2 * kStride);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i)
+    if (warp == i && i < n_rounds) request(look_up(i), use + i);
 
   // q in the order of the key words, times a power of two per row; sums of its rows
-  uint32_t qf[NT][2 * KW][2];
-  float sumq[NT][2], rowf[NT][2];
-  int lim[NT][2];
+  State<D, NT> S;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int row = row_first + 8 * j + r, tok = row / G;
@@ -348,185 +490,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
         v[2 * i] = __uint_as_float(e[i] << 16);
         v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
       }
-      qf[j][2 * w][0] = pack_half2(v[0] * fe, v[4] * fe);
-      qf[j][2 * w][1] = pack_half2(v[1] * fo, v[5] * fo);
-      qf[j][2 * w + 1][0] = pack_half2(v[2] * fe, v[6] * fe);
-      qf[j][2 * w + 1][1] = pack_half2(v[3] * fo, v[7] * fo);
+      S.qf[j][2 * w][0] = pack_half2(v[0] * fe, v[4] * fe);
+      S.qf[j][2 * w][1] = pack_half2(v[1] * fo, v[5] * fo);
+      S.qf[j][2 * w + 1][0] = pack_half2(v[2] * fe, v[6] * fe);
+      S.qf[j][2 * w + 1][1] = pack_half2(v[3] * fo, v[7] * fo);
     }
     const float back = exp2i(min(127, 24 - 14 + ex)) * p.scale_log2;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4) * p.scale_log2;
-      rowf[j][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
+      S.sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4) * p.scale_log2;
+      S.rowf[j][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
       const int rw = row_first + 8 * j + 2 * t + e;
-      lim[j][e] = rw < rows ? min(end, q.len - q.n + rw / G + 1) : 0;
+      S.lim[j][e] = rw < rows ? min(end, q.len - q.n + rw / G + 1) : 0;
     }
   }
 
-  float o[NT][MT][4], m[NT][2], l[NT][2], corr[NT][2];
+  int lim_all = INT_MAX;  // positions that every row of the tile sees
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+    for (int i = 0; i < MT; ++i) S.o[j][i][0] = S.o[j][i][1] = S.o[j][i][2] = S.o[j][i][3] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[j][e] = -INFINITY, l[j][e] = 0.f, corr[j][e] = 0.f;
+    for (int e = 0; e < 2; ++e) S.m[j][e] = -INFINITY, S.l[j][e] = 0.f, S.corr[j][e] = 0.f;
   }
-  int ve = 1;  // exponent field of the largest value scale so far; weights carry 2^(28 - ve)
-  const int tr = (r >> 1) + 4 * (r & 1);  // the token of score row r (and of row r + 8: tr + 8)
+  lim_all = min(end, q.len - q.n + row_first / G + 1);
+  S.ve = 1;
 
-  for (int stage = 0; t0 < end; t0 += kStride) {
-    copy_wait<1>();
+  for (int i = 0; i < n_rounds; ++i, ++use) {
+    const int stage = use % kStages;
+    const bool duty = i + kStages - 1 < n_rounds && (use + kStages - 1) % kWarps == warp;
+    int page = -2;
+    if (duty) page = look_up(i + kStages - 1);
+    wait(&sm.full[stage], (uint32_t)(use / kStages) & 1u);
+    const int pos0 = begin + i * kRound + kStep * warp;
+    if (pos0 < end && !*abort) {
+      const uint32_t at_stage = (uint32_t)stage * (uint32_t)sizeof(sm.ring[0]), there = sm.there[stage];
+      const uint32_t kb[2] = {okb[0] + at_stage, okb[1] + at_stage}, vb[2] = {ovb[0] + at_stage, ovb[1] + at_stage},
+                     pb[2] = {opb[0] + at_stage, opb[1] + at_stage};
+      const bool g0 = (there >> page_bit[0]) & 1u, g1 = (there >> page_bit[1]) & 1u;
+      const int stop[2] = {g0 ? end : 0, g1 ? end : 0};
+      if (g0 && g1 && pos0 + kStep <= lim_all)
+        step<D, NT, true>(S, pos0, kb, vb, pb, stop, tr, tx);
+      else
+        step<D, NT, false>(S, pos0, kb, vb, pb, stop, tr, tx);
+    }
     __syncwarp();
-    // the stage that the previous step has read
-    const int spare = stage == 0 ? kStages - 1 : stage - 1;
-    there |= issue(t0 + 2 * kStride, spare) << 4;
-    look_up(t0 + 3 * kStride);
-
-    float sc[2][NT][4];
-    float2 vs[2][2];
-    unsigned vbig = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int pos = t0 + 16 * g;
-      const uint32_t kb = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes;
-      uint32_t ka[KW], kc[KW], pa[2], pb[2];
-      const uint32_t kp = D == 128 ? piece<D>(tr, t) : piece<D>(tr, t >> 1) + (t & 1) * 8;
-      lds_words<KW>(ka, kb + kp);
-      lds_words<KW>(kc, kb + kp + Group<D>::kCodes / 2);  // eight tokens on
-      lds_words<2>(pa, kb + 2 * Group<D>::kCodes + tr * 8);
-      lds_words<2>(pb, kb + 2 * Group<D>::kCodes + tr * 8 + 64);
-      vs[g][0] = half2_at(pa[1]);
-      vs[g][1] = half2_at(pb[1]);
-      const int stop = (there >> g) & 1u ? end : 0;
-      if (pos + tr < stop) vbig = max(vbig, pa[1] & 0xFFFFu);
-      if (pos + tr + 8 < stop) vbig = max(vbig, pb[1] & 0xFFFFu);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sc[g][j][0] = sc[g][j][1] = sc[g][j][2] = sc[g][j][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const uint32_t a8 = ka[w] >> 8, c8 = kc[w] >> 8;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_f16(sc[g][j], even4(ka[w]), even4(kc[w]), odd4(ka[w]), odd4(kc[w]), qf[j][2 * w][0], qf[j][2 * w][1]);
-          mma_f16(sc[g][j], even4(a8), even4(c8), odd4(a8), odd4(c8), qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
-        }
-      }
-      const float2 k0 = half2_at(pa[0]), k1 = half2_at(pb[0]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int seen = min(stop, lim[j][e]);
-          sc[g][j][e] = pos + tr < seen ? fmaf(k0.x * sc[g][j][e], rowf[j][e], k0.y * sumq[j][e]) : -INFINITY;
-          sc[g][j][2 + e] =
-              pos + tr + 8 < seen ? fmaf(k1.x * sc[g][j][2 + e], rowf[j][e], k1.y * sumq[j][e]) : -INFINITY;
-        }
-      }
-    }
-    // running maxima; the accumulators are scaled only when one has grown
-    const int ve2 = max(ve, (int)(__reduce_max_sync(0xffffffffu, vbig) >> 10));
-    float ref[NT][2];
-    bool grown = ve2 > ve;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(sc[0][j][e], sc[0][j][2 + e]), fmaxf(sc[1][j][e], sc[1][j][2 + e]));
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-        grown |= x > m[j][e];
-        ref[j][e] = fmaxf(x, m[j][e]);
-      }
-    }
-    if (__any_sync(0xffffffffu, grown)) {
-      const float fv = exp2i(ve - ve2);
-      ve = ve2;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float f[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f[e] = m[j][e] == -INFINITY ? 0.f : ex2(m[j][e] - ref[j][e]);
-          m[j][e] = ref[j][e];
-          l[j][e] *= f[e];
-          corr[j][e] *= f[e];
-          f[e] *= fv;
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          o[j][i][0] *= f[0];
-          o[j][i][1] *= f[1];
-          o[j][i][2] *= f[0];
-          o[j][i][3] *= f[1];
-        }
-      }
-    }
-    const float vf = exp2i(28 - ve);
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float vsc = vs[g][k].x * vf;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float w[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = sc[g][j][2 * k + e];
-            const bool in = x != -INFINITY;  // a masked place takes no part, whatever its scales hold
-            const float pr = in ? ex2(x - m[j][e]) : 0.f;
-            l[j][e] += pr;
-            w[e] = in ? pr * vsc : 0.f;
-            if (in) corr[j][e] = fmaf(pr, vs[g][k].y, corr[j][e]);
-          }
-          pb[j][k] = transpose8x8(pack_half2(w[0], w[1]));
-        }
-      }
-      uint32_t vw[4][VW];
-      const uint32_t vb = ring + (uint32_t)(stage * 2 + g) * Group<D>::kBytes + Group<D>::kCodes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        lds_words<VW>(vw[i], vb + (D == 128 ? piece<D>(t + 4 * i, r >> 1) + (r & 1) * 8
-                                            : piece<D>(t + 4 * i, r >> 2) + (r & 3) * 4));
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t a[2] = {lo16(vw[0][w], vw[1][w]), hi16(vw[0][w], vw[1][w])};
-        const uint32_t b[2] = {lo16(vw[2][w], vw[3][w]), hi16(vw[2][w], vw[3][w])};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a8 = a[i] >> 8, b8 = b[i] >> 8;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_f16(o[j][4 * w + 2 * i], even4(a[i]), odd4(a[i]), even4(b[i]), odd4(b[i]), pb[j][0], pb[j][1]);
-            mma_f16(o[j][4 * w + 2 * i + 1], even4(a8), odd4(a8), even4(b8), odd4(b8), pb[j][0], pb[j][1]);
-          }
-        }
-      }
-    }
-    there >>= 2;
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+    if (lane == 0) tc::mbar_arrive(&sm.empty[stage]);
+    if (duty) request(page, use + kStages - 1);
   }
-  copy_wait<0>();
-  __syncthreads();  // the rings become the exchange of the states
+  __syncthreads();  // the ring becomes the exchange of the states
 
   // the warps' states: codes were c 2^-24 and c 2^-20, weights carried 2^(28 - ve)
-  const float back_even = exp2i(24 - 28 + ve), back_odd = exp2i(20 - 28 + ve);
+  const float back_even = exp2i(24 - 28 + S.ve), back_odd = exp2i(20 - 28 + S.ve);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) {
-        l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], k);
-        corr[j][e] += __shfl_xor_sync(0xffffffffu, corr[j][e], k);
+        S.l[j][e] += __shfl_xor_sync(0xffffffffu, S.l[j][e], k);
+        S.corr[j][e] += __shfl_xor_sync(0xffffffffu, S.corr[j][e], k);
       }
       const int n = 8 * j + 2 * t + e;
-      if (r == 0) sm.m[warp][n] = m[j][e], sm.l[warp][n] = l[j][e];
+      if (r == 0) sm.m[warp][n] = S.m[j][e], sm.l[warp][n] = S.l[j][e];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         *reinterpret_cast<float2*>(&sm.o[warp][n][r * (D / 8) + 2 * i]) =
-            make_float2(fmaf(o[j][i][e], back_even, corr[j][e]), fmaf(o[j][i][2 + e], back_odd, corr[j][e]));
+            make_float2(fmaf(S.o[j][i][e], back_even, S.corr[j][e]), fmaf(S.o[j][i][2 + e], back_odd, S.corr[j][e]));
     }
   }
   __syncthreads();
@@ -610,9 +640,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
       }
     }
   }
-  __syncthreads();  // the exchange becomes the rings again
+  fence_proxy_async_smem();
+  __syncthreads();  // the exchange becomes the ring again
   }
   }
+  if (*abort && threadIdx.x == 0)  // no copy of this CTA's may be under way when it ends
+    for (int i = 0; i < kStages; ++i)
+      if (sm.phase[i] < 2) mbar_wait_bounded(&sm.full[i], sm.phase[i]);
 }
 
 template <int D, int NT>
@@ -629,7 +663,7 @@ int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
 // with 8 rows, one with more (registers), and no more CTAs than rounds.
 tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int max_len, int sms, Kv4AttnPlan* pl) {
   const long long rows = (long long)max_new * (heads / c.kv_heads);
-  if (rows > (1 << 30)) return TERN_EUNSUPPORTED;
+  if (rows > (1 << 30) || max_len > (1 << 30)) return TERN_EUNSUPPORTED;
   pl->rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   const long long tiles = (rows + pl->rows - 1) / pl->rows, rounds = std::max(1, (max_len - 1) / kRound + 1);
   // seqs x kv_heads x tiles x rounds must stay below 2^63 / kMaxCtas in the kernel
