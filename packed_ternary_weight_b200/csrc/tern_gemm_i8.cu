@@ -1,15 +1,34 @@
 // 8-bit product with a scale per token and output channel:
-//   y[m][n] = fl(fl(fl(acc) w_scale[n]) x_scale[m]), acc = sum_k w[n][k] x[m][k] exactly.
+//   y[m][n] = fl(fl(fl(acc) w_scale[n]) x_scale[m]), acc = sum_k w[n][k] x[m][k] exactly,
+// on the 5th-generation tensor cores (tcgen05 kind::i8, int32 accumulators in
+// tensor memory).
 //
-// Each warp takes four output channels and up to eight tokens; its lanes
-// stride over k in 16-byte pieces with byte dot products.
+// The weights are the A operand (128 channels per tile) and the tokens the B
+// operand (N = 16..256 of them per tile, the count padded to 16), so that one
+// kernel serves a single token, where it streams weights, and a prompt, where it
+// is bound by the tensor cores; and so that a thread of the epilogue holds one
+// channel and a warp writes 32 consecutive channels of a token.
+//
+// One persistent CTA per SM:
+//   warp 0     tensor-map loads of A and B steps (128 bytes of K, 128-byte
+//              swizzle) into a ring as deep as shared memory allows; K, rows and
+//              tokens beyond the ends arrive as zeros;
+//   warp 1     one thread issues the MMAs and commits them to mbarriers;
+//   warps 4-7  read the accumulators (two buffers, so that the next tile's MMAs
+//              run meanwhile), scale and store.
+// Fewer tiles than SMs: the steps of a tile are dealt to a cluster of 2, 4 or 8
+// CTAs, whose exact int32 partial sums meet in distributed shared memory; each
+// CTA of the cluster finishes a share of the tokens. Integer sums: the result
+// does not depend on the split.
+// Every wait is bounded; on expiry the device error word records a timeout and
+// the CTA runs to its end without waiting further.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "tern_internal.h"
-#include "tern_ptx.cuh"
+#include "tern_tc.cuh"
 
 namespace tern {
 
@@ -17,61 +36,276 @@ int read_clear_dev_error_gemm_i8(void* stream, unsigned* out) { return read_clea
 
 namespace {
 
-constexpr int kRows = 4, kTok = 8;
+constexpr int kThreads = 256;
+constexpr int kRowsA = 128;               // channels per tile
+constexpr int kStepK = 128;               // bytes of K per step
+constexpr int kBytesA = kRowsA * kStepK;  // 16 KB
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplit = 8;
+constexpr int kSmemTop = 227 * 1024;
 
-// 16 bytes of a row, zero from `left` bytes on
-__device__ __forceinline__ int4 mask16(int4 v, int left) {
-  if (left >= 16) return v;
-  int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = left - 4 * i;
-    w[i] = b >= 4 ? w[i] : (b <= 0 ? 0 : w[i] & (int)((1u << (8 * b)) - 1u));
-  }
-  return make_int4(w[0], w[1], w[2], w[3]);
+struct Plan {
+  int tn, tiles_n, tiles_m, tiles;  // tokens per tile; tiles of channels, of tokens
+  int steps, split;                 // of K; CTAs that share a tile
+  int stages, stage_bytes, grid;
+  uint32_t tmem_cols;
+};
+
+struct Args {
+  GemmI8Params p;
+  Plan pl;
+};
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], fin;
+  uint32_t misc[4];  // tensor-memory base, abort flag
+  float sx[2][256];
+};
+constexpr int kCtlBytes = 3 * 1024;
+static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
+
+__device__ __forceinline__ void named_sync_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ uint32_t ld_dsmem(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-__global__ void __launch_bounds__(256) dot_kernel(const GemmI8Params p) {
-  const int lane = threadIdx.x & 31;
-  const int n0 = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)) * kRows, m0 = (int)blockIdx.y * kTok;
-  if (n0 >= p.n) return;
-  int acc[kRows][kTok] = {};
-  for (int k = lane * 16; k < p.k; k += 512) {
-    int4 w[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      w[i] = mask16(*reinterpret_cast<const int4*>(p.w + (int64_t)min(n0 + i, p.n - 1) * p.ldw + k), p.k - k);
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      if (m0 + j >= p.m) break;
-      const int4 x = *reinterpret_cast<const int4*>(p.x + (int64_t)(m0 + j) * p.ldx + k);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        acc[i][j] = __dp4a(w[i].x, x.x, __dp4a(w[i].y, x.y, __dp4a(w[i].z, x.z, __dp4a(w[i].w, x.w, acc[i][j]))));
+__device__ __forceinline__ void store_one(const GemmI8Params& p, int m, int n, int acc, float sw, float sx) {
+  const float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), sw), sx);
+  const int64_t at = (int64_t)m * p.ldy + n;
+  if (p.out_bf16)
+    static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(p.y)[at] = v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_i8_kernel(const Args a, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const GemmI8Params& p = a.p;
+  const Plan& pl = a.pl;
+  // the dynamic block need not start on a swizzle atom
+  const uint32_t base = smem_u32(smem), pad = (1024u - (base & 1023u)) & 1023u;
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + pad);
+  const uint32_t ring = base + pad + kCtlBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile uint32_t* misc = ctl.misc;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.acc_full[i], 1);
+      mbar_init(&ctl.acc_empty[i], 4);
+    }
+    mbar_init(&ctl.fin, 1);
+    ctl.misc[tc::kMiscAbort] = 0;
+    fence_mbar_init();
   }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      const int v = __reduce_add_sync(0xffffffffu, acc[i][j]);
-      if (lane == i * kTok + j && n0 + i < p.n && m0 + j < p.m) {
-        const float y = __fmul_rn(__fmul_rn(__int2float_rn(v), p.wscale[n0 + i]), p.xscale[m0 + j]);
-        const int64_t at = (int64_t)(m0 + j) * p.ldy + n0 + i;
-        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(y);
-        else static_cast<float*>(p.y)[at] = y;
+  if (warp == 1) {
+    tc::tmem_alloc(smem_u32(&ctl.misc[tc::kMiscTmem]), pl.tmem_cols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl.misc[tc::kMiscTmem];
+  // a tile's CTAs are a cluster of pl.split consecutive ones
+  const int rank = pl.split > 1 ? (int)(blockIdx.x % pl.split) : 0;
+  const int first = (int)blockIdx.x / pl.split, stride = (int)gridDim.x / pl.split;
+  const int k0 = pl.steps * rank / pl.split, k1 = pl.steps * (rank + 1) / pl.split;  // at least one step each
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t ph = 0;
+      for (int tile = first; tile < pl.tiles && !misc[tc::kMiscAbort]; tile += stride) {
+        const int n0 = (tile % pl.tiles_n) * kRowsA, m0 = (tile / pl.tiles_n) * pl.tn;
+        for (int k = k0; k < k1; ++k) {
+          if (issued >= pl.stages && !tc::tc_wait(&ctl.empty[stage], ph ^ 1u, misc)) break;
+          const uint32_t st = ring + (uint32_t)(stage * pl.stage_bytes);
+          mbar_arrive_expect_tx(&ctl.full[stage], (uint32_t)(kBytesA + pl.tn * kStepK));
+          tc::tma_load_2d(st, &map_w, k * kStepK, n0, &ctl.full[stage]);
+          tc::tma_load_2d(st + kBytesA, &map_x, k * kStepK, m0, &ctl.full[stage]);
+          ++issued;
+          if (++stage == pl.stages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (misc[tc::kMiscAbort]) {  // no load may be under way when the CTA ends
+        for (int i = 0; i < min(issued, pl.stages); ++i) {
+          if (--stage < 0) {
+            stage = pl.stages - 1;
+            ph ^= 1u;
+          }
+          mbar_wait_bounded(&ctl.full[stage], ph);
+        }
       }
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_i8_s32(pl.tn);
+      int stage = 0, seg = 0;
+      uint32_t ph = 0;
+      for (int tile = first; tile < pl.tiles && !misc[tc::kMiscAbort]; tile += stride, ++seg) {
+        const int buf = seg & 1;
+        if (seg >= 2 && !tc::tc_wait(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u, misc)) break;
+        tc::fence_after_sync();
+        const uint32_t acc = tmem + (uint32_t)(buf * pl.tn);
+        for (int k = k0; k < k1; ++k) {
+          if (!tc::tc_wait(&ctl.full[stage], ph, misc)) break;
+          tc::fence_after_sync();
+          const uint32_t st = ring + (uint32_t)(stage * pl.stage_bytes);
+          const uint64_t ad = tc::smem_desc_sw128(st), bd = tc::smem_desc_sw128(st + kBytesA);
+#pragma unroll
+          for (int i = 0; i < kStepK / 32; ++i)  // 32 bytes of K: two 16-byte units of the start address
+            tc::mma_i8(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u);
+          tc::commit(&ctl.empty[stage]);
+          if (++stage == pl.stages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        tc::commit(&ctl.acc_full[buf]);
+      }
+      // every MMA issued has completed before tensor memory is released
+      tc::commit(&ctl.fin);
+      mbar_wait_bounded(&ctl.fin, 0u);
+    }
+  } else if (warp >= 4) {
+    const int q4 = warp & 3, et = threadIdx.x - 128;
+    const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+    int seg = 0;
+    for (int tile = first; tile < pl.tiles; tile += stride, ++seg) {
+      const int buf = seg & 1;
+      const int n = (tile % pl.tiles_n) * kRowsA + 32 * q4 + lane, m0 = (tile / pl.tiles_n) * pl.tn;
+      const int cols = min(pl.tn, p.m - m0);
+      float* sx = ctl.sx[buf];
+      for (int i = et; i < cols; i += 128) sx[i] = __ldg(p.xscale + m0 + i);
+      const float sw = n < p.n ? __ldg(p.wscale + n) : 0.f;
+      named_sync_epilogue();
+      tc::tc_wait_many(&ctl.acc_full[buf], (uint32_t)(seg / 2) & 1u, misc);
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + (uint32_t)(buf * pl.tn) + lanes;
+      for (int c = 0; c < pl.tn; c += 16) {
+        uint32_t v[16];
+        tc::ld_x16_sync(acc + (uint32_t)c, v);
+        if (pl.split > 1) {  // [token][channel] at the ring's start: the loads are all in, and read
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + (uint32_t)((c + i) * kRowsA + 32 * q4 + lane) * 4u),
+                         "r"(v[i])
+                         : "memory");
+        } else if (n < p.n) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < cols) store_one(p, m0 + c + i, n, (int)v[i], sw, sx[c + i]);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl.acc_empty[buf]);
+    }
   }
+  __syncthreads();
+  if (pl.split > 1) {
+    // the cluster's partial sums, a share of the tokens per CTA
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_wait_acquire();
+    const int n0 = (first % pl.tiles_n) * kRowsA, m0 = (first / pl.tiles_n) * pl.tn;
+    const int cols = min(pl.tn, p.m - m0);
+    const int n = n0 + (int)(threadIdx.x & 127);
+    if (n < p.n) {
+      const float sw = __ldg(p.wscale + n);
+      for (int c = rank + pl.split * (int)(threadIdx.x >> 7); c < cols; c += 2 * pl.split) {
+        const uint32_t at = ring + (uint32_t)(c * kRowsA + (int)(threadIdx.x & 127)) * 4u;
+        int acc = 0;
+#pragma unroll 8
+        for (int r = 0; r < pl.split; ++r) acc += (int)ld_dsmem(map_cluster_rank(at, (uint32_t)r));
+        store_one(p, m0 + c, n, acc, sw, __ldg(p.xscale + m0 + c));
+      }
+    }
+    __syncwarp();
+    cluster_arrive_relaxed();  // a CTA's shared memory stays until its peers have read it
+    cluster_wait_acquire();
+  }
+  if (warp == 1) tc::tmem_dealloc(tmem, pl.tmem_cols);
+}
+
+// Tokens per tile: the fewest tiles of up to 256, of equal size. Fewer tiles
+// than SMs: split K over a cluster, as long as every CTA keeps four steps.
+Plan make_plan(int m, int n, int k, int sms) {
+  Plan pl{};
+  pl.tiles_m = (m + 255) / 256;
+  pl.tn = ((m + pl.tiles_m - 1) / pl.tiles_m + 15) / 16 * 16;
+  pl.tiles_m = (m + pl.tn - 1) / pl.tn;
+  pl.tiles_n = (n + kRowsA - 1) / kRowsA;
+  pl.steps = (k + kStepK - 1) / kStepK;
+  const long long tiles = (long long)pl.tiles_n * pl.tiles_m;
+  pl.tiles = (int)std::min(tiles, 0x7FFFFFFFll);
+  pl.split = 1;
+  while (pl.split < kMaxSplit && tiles * pl.split * 2 <= sms && pl.steps >= pl.split * 2 * 4) pl.split *= 2;
+  pl.stage_bytes = kBytesA + pl.tn * kStepK;
+  pl.stages = std::min(kMaxStages, (kSmemTop - 1024 - kCtlBytes) / pl.stage_bytes);
+  pl.grid = (int)std::min<long long>(tiles * pl.split, pl.split > 1 ? tiles * pl.split : sms);
+  pl.tmem_cols = 32;
+  while (pl.tmem_cols < 2u * (uint32_t)pl.tn) pl.tmem_cols *= 2;
+  return pl;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &st) != cudaSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* map, const int8_t* base, int k, int rows, int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {(cuuint32_t)kStepK, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  EncodeTiled fn = encoder();
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
-  (void)sms;
-  const dim3 grid((unsigned)((p.n + 8 * kRows - 1) / (8 * kRows)), (unsigned)((p.m + kTok - 1) / kTok));
-  dot_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return (int)cudaGetLastError();
+  Args a{p, make_plan(p.m, p.n, p.k, sms)};
+  CUtensorMap mw, mx;
+  if (!encode(&mw, p.w, p.k, p.n, p.ldw, kRowsA) || !encode(&mx, p.x, p.k, p.m, p.ldx, a.pl.tn)) return -1;
+  const int bytes = kSmemTop;
+  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return (int)e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)a.pl.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  if (a.pl.split > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)a.pl.split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  e = cudaLaunchKernelEx(&cfg, gemm_i8_kernel, a, mw, mx);
+  return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 
 }  // namespace tern
@@ -83,7 +317,7 @@ extern "C" tern_status tern_gemm_i8(int32_t m, int32_t n, int32_t k, const int8_
   if (m < 0 || n < 1 || k < 1 || k > 131071 || ldx < k || ldw < k || ldy < n || ((ldx | ldw) & 15) != 0)
     return TERN_EINVAL;
   if (out != TERN_OUT_F32 && out != TERN_OUT_BF16) return TERN_EINVAL;
-  if (m > 65535 * 8) return TERN_EINVAL;
+  if ((int64_t)((m + 15) / 16) * ((n + 127) / 128) > 0x7FFFFFFFll) return TERN_EINVAL;
   if (m == 0) return TERN_OK;
   if (!d_x || !d_xscale || !d_w || !d_wscale || !d_y) return TERN_EINVAL;
   if (((reinterpret_cast<uintptr_t>(d_x) | reinterpret_cast<uintptr_t>(d_w)) & 15u) != 0) return TERN_EALIGN;
@@ -104,5 +338,6 @@ extern "C" tern_status tern_gemm_i8(int32_t m, int32_t n, int32_t k, const int8_
   p.n = n;
   p.k = k;
   p.out_bf16 = out == TERN_OUT_BF16;
-  return launch_gemm_i8(p, sm_count(), stream) == 0 ? TERN_OK : TERN_ECUDA;
+  const int rc = launch_gemm_i8(p, sm_count(), stream);
+  return rc == 0 ? TERN_OK : TERN_ECUDA;
 }

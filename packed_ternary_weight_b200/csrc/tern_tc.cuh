@@ -46,6 +46,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t addr, uint32_t sbo) 
          (4ull << 61);
 }
 
+// Shared-memory matrix descriptor, 128-byte swizzle, K-major: rows of 128
+// bytes, 8-row atoms of 1024 bytes (16-byte chunk c of row r stored at chunk
+// c ^ (r & 7)), as a tensor-map load with the same swizzle writes them; swizzle
+// mode 2 at bits 61-63. The atom base must be 1024-byte aligned; a K offset
+// inside the 128-byte row is added to the start.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
 // Instruction descriptor of kind::i8 with signed A and B, int32 accumulator,
 // both operands K-major, M = 128 rows, N columns (16..256, multiple of 16).
 __host__ __device__ constexpr uint32_t idesc_i8_s32(int n) {
@@ -79,6 +89,18 @@ __device__ __forceinline__ void ld_x8_sync(uint32_t taddr, uint32_t (&v)[8]) {
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Sixteen consecutive 32-bit columns of this warp's lane quarter, as ld_x8_sync.
+__device__ __forceinline__ void ld_x16_sync(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
 }
@@ -160,6 +182,16 @@ __device__ __forceinline__ void bulk_g2s_plain(uint32_t dst_smem, const void* sr
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_smem),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Two-dimensional tensor-map load: the box at (x, y), x a multiple of 16 bytes;
+// places outside the tensor arrive as zeros and count.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst_smem, const void* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst_smem),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
 
