@@ -646,6 +646,7 @@ extern "C" tern_status tern_device_error(void* stream) {
   if (read_clear_dev_error_decode(stream, &v) != 0) return TERN_ECUDA;
   if (read_clear_dev_error_kv4(stream, &v) != 0) return TERN_ECUDA;
   if (read_clear_dev_error_kv4_attn(stream, &v) != 0) return TERN_ECUDA;
+  if (read_clear_dev_error_kv4_prompt(stream, &v) != 0) return TERN_ECUDA;
   if (read_clear_dev_error_gemm_i8(stream, &v) != 0) return TERN_ECUDA;
   if (v & TERN_DEVERR_TIMEOUT) return TERN_ETIMEOUT;
   return v ? TERN_EFORMAT : TERN_OK;

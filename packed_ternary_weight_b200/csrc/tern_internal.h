@@ -350,23 +350,36 @@ struct Kv4ReadParams {
 int launch_kv4_read(const Kv4ReadParams& p, void* stream);
 int read_clear_dev_error_kv4(void* stream, unsigned* out);
 
-// Launch plan of the attention over few query rows: `rows` query rows per CTA
-// (8, 16 or 32) and the number of CTAs.
-struct Kv4AttnPlan {
-  int rows, ctas;
-  size_t cnt_bytes, ws_bytes;
-};
+// Attention over few query rows per sequence and kv head (up to max_rows; others
+// are left to the prompt kernel).
 struct Kv4AttnParams {
   Kv4Params c;
   const uint16_t* q;
   uint16_t* out;
   float scale_log2;           // scale * log2(e)
   int group;                  // query heads per kv head
+  int max_rows;
   unsigned* cnt;              // [CTAs], zero on entry and exit
   float* part;                // [CTAs][2][rows * (dim + 2)]
 };
-int launch_kv4_attn(const Kv4AttnParams& p, const Kv4AttnPlan& plan, void* stream);
+int launch_kv4_attn(const Kv4AttnParams& p, int rows, int ctas, void* stream);  // rows per CTA: 8 or 16
 int read_clear_dev_error_kv4_attn(void* stream, unsigned* out);
+
+// Attention over sequences with min_rows query rows per kv head or more.
+struct Kv4PromptParams {
+  Kv4Params c;
+  const uint16_t* q;
+  uint16_t* out;
+  float scale_log2;
+  int group;
+  int min_rows;
+  long long min_share;        // blocks of 128 positions a CTA takes at least
+  unsigned* cnt;              // [CTAs], zero on entry and exit
+  float* part;                // [CTAs][2][256 * (dim + 2)]
+};
+size_t kv4_prompt_part_bytes(int dim, int ctas);
+int launch_kv4_prompt(const Kv4PromptParams& p, int ctas, void* stream);
+int read_clear_dev_error_kv4_prompt(void* stream, unsigned* out);
 
 struct GemmI8Params {
   const int8_t* x;

@@ -36,6 +36,87 @@ __device__ __forceinline__ int page_of(const Kv4Params& c, int s, int pos) {
   return (unsigned)id < (unsigned)c.num_pages ? id : -1;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// The batch's work as one line of rounds, sequence after sequence; CTA c of
+// `ctas` takes the rounds [total c / ctas, total (c + 1) / ctas), at least
+// min_share of them where there are as many. Every thread of the CTA calls
+// find_share; weight(s, report) is the number of rounds of sequence s.
+struct Share {
+  long long total, ctas, at, stop;
+  int s;             // the sequence of round `at`
+  long long in_seq;  // rounds of it before `at`
+  // the CTA that holds round x
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * ctas - 1) / total); }
+};
+template <int WARPS>
+struct ShareScratch {
+  long long scan[WARPS], off;
+  int found;
+};
+template <int WARPS, typename Weight>
+__device__ __forceinline__ bool find_share(int seqs, long long min_share, Weight weight, ShareScratch<WARPS>& sm,
+                                           Share* out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long total = 0;
+  if (seqs == 1) {
+    total = weight(0, blockIdx.x == 0 && threadIdx.x == 0);
+  } else {
+    long long v = 0;
+    for (int i = threadIdx.x; i < seqs; i += 32 * WARPS) v += weight(i, blockIdx.x == 0);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    if (lane == 0) sm.scan[warp] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) total += sm.scan[i];
+    __syncthreads();
+  }
+  const long long ctas = min((long long)gridDim.x, max(min(total, 1ll), total / min_share));
+  if (blockIdx.x >= ctas) return false;
+  out->total = total;
+  out->ctas = ctas;
+  out->at = total * blockIdx.x / ctas;
+  out->stop = total * (blockIdx.x + 1) / ctas;
+  out->s = 0;
+  out->in_seq = out->at;
+  if (seqs == 1) return true;
+  long long before = 0;
+  for (int base = 0; base < seqs; base += 32 * WARPS) {
+    const int i = base + threadIdx.x;
+    const long long w = i < seqs ? weight(i, false) : 0;
+    long long incl = w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, k);
+      if (lane >= k) incl += v;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    if (threadIdx.x == 0) sm.found = -1;
+    __syncthreads();
+    long long pre = before;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      if (k < warp) pre += sm.scan[k];
+      before += sm.scan[k];
+    }
+    if (out->at >= pre + incl - w && out->at < pre + incl) {
+      sm.found = i;
+      sm.off = out->at - (pre + incl - w);
+    }
+    __syncthreads();
+    if (sm.found >= 0) break;
+  }
+  out->s = sm.found;
+  out->in_seq = sm.off;
+  return out->s >= 0;  // not found: the lengths changed meanwhile
+}
+
 }  // namespace kv4
 
 // Host: argument checks that every call on the cache shares (batch may be NULL).

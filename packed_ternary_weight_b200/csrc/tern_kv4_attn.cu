@@ -73,11 +73,9 @@ constexpr int kStages = 3;  // rounds in the ring
 constexpr int kRound = kStep * kWarps;  // positions of a CTA's round
 constexpr int kMaxCtas = 512;           // of a launch
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+using kv4::ex2;
+using kv4::exp2i;
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -101,7 +99,6 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 template <int WORDS>
 __device__ __forceinline__ void lds_words(uint32_t (&v)[WORDS], uint32_t a) {
@@ -131,9 +128,7 @@ struct Shared {
   uint32_t there[kStages];                 // pages of a stage that are in the cache, one bit each
   uint32_t phase[kStages];                 // of a stage's last request; 2: none yet
   uint32_t abort;                          // a bounded wait has given up
-  long long scan[kWarps + 1];              // the search for the CTA's first round
-  long long found_off;
-  int found;
+  kv4::ShareScratch<kWarps> share;
   int last;
 };
 
@@ -142,7 +137,7 @@ __device__ __forceinline__ long long rounds_of(const Kv4AttnParams& p, const kv4
                                                int* rounds) {
   *tiles = (q.n * p.group + R - 1) / R;
   *rounds = max(1, (q.len + kRound - 1) / kRound);
-  return q.ok ? (long long)p.c.kv_heads * *tiles * *rounds : 0;
+  return q.ok && q.n * p.group <= p.max_rows ? (long long)p.c.kv_heads * *tiles * *rounds : 0;
 }
 
 __device__ __forceinline__ void store_row(const Kv4AttnParams& p, const kv4::Seq& q, int D, int h, int row, int d,
@@ -338,72 +333,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
     opb[g] = blk + (uint32_t)c.page * D + (uint32_t)(slot + tr) * 8;
   }
 
-  // this CTA's rounds [at, stop_at) and the sequence and place of the first
-  long long total, ctas, at, stop_at;
-  int s = 0;
-  long long in_seq;  // rounds of sequence s before `at`
-  {
+  kv4::Share sh;
+  auto weight = [&](int i, bool report) -> long long {
+    const kv4::Seq q = kv4::load_seq(c, i);
+    if (!q.ok && report) kv4::report_bad();
     int tiles, rounds;
-    auto weight = [&](int i, bool report) -> long long {
-      const kv4::Seq q = kv4::load_seq(c, i);
-      if (!q.ok && report) kv4::report_bad();
-      return rounds_of(p, q, R, &tiles, &rounds);
-    };
-    auto block_sum = [&](long long v) {
-#pragma unroll
-      for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-      if (lane == 0) sm.scan[warp] = v;
-      __syncthreads();
-      long long all = 0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) all += sm.scan[i];
-      __syncthreads();
-      return all;
-    };
-    if (c.seqs == 1) {
-      total = weight(0, blockIdx.x == 0 && threadIdx.x == 0);
-    } else {
-      long long mine = 0;
-      for (int i = threadIdx.x; i < c.seqs; i += kThreads) mine += weight(i, blockIdx.x == 0);
-      total = block_sum(mine);
-    }
-    ctas = min((long long)gridDim.x, total);  // each of them holds a round
-    if (blockIdx.x >= ctas) return;
-    at = total * blockIdx.x / ctas;
-    stop_at = total * (blockIdx.x + 1) / ctas;
-    in_seq = at;
-    if (c.seqs > 1) {
-      long long before = 0;
-      for (int base = 0; base < c.seqs; base += kThreads) {
-        const int i = base + threadIdx.x;
-        const long long w = i < c.seqs ? weight(i, false) : 0;
-        long long incl = w;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, k);
-          if (lane >= k) incl += v;
-        }
-        if (lane == 31) sm.scan[warp] = incl;
-        if (threadIdx.x == 0) sm.found = -1;
-        __syncthreads();
-        long long pre = before;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          if (k < warp) pre += sm.scan[k];
-          before += sm.scan[k];
-        }
-        if (at >= pre + incl - w && at < pre + incl) {
-          sm.found = i;
-          sm.found_off = at - (pre + incl - w);
-        }
-        __syncthreads();
-        if (sm.found >= 0) break;
-      }
-      s = sm.found;
-      in_seq = sm.found_off;
-      if (s < 0) return;  // the lengths changed meanwhile
-    }
-  }
+    return rounds_of(p, q, R, &tiles, &rounds);
+  };
+  if (!kv4::find_share<kWarps>(c.seqs, 1, weight, sm.share, &sh)) return;
+  int s = sh.s;
+  long long at = sh.at, in_seq = sh.in_seq;
+  const long long stop_at = sh.stop;
 
   const uint64_t policy = policy_evict_first();
   int use = 0;  // rounds this CTA has taken
@@ -561,8 +501,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
   }
   __syncthreads();
   // the tile's CTAs: the first holds its first round, the last its last
-  const int first_cta = (int)(((unit_first + 1) * ctas - 1) / total);
-  const int last_cta = (int)(((unit_first + rounds) * ctas - 1) / total);
+  const int first_cta = sh.cta_of(unit_first), last_cta = sh.cta_of(unit_first + rounds - 1);
   const bool whole = first_cta == last_cta;
   constexpr int kSlot = R * (D + 2);  // floats: weighted values [R][D], then (maximum, sum) [R]
   float* part = p.part + (size_t)(2 * blockIdx.x + (round0 == 0 ? 1 : 0)) * kSlot;
@@ -658,38 +597,53 @@ int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
   return (int)cudaGetLastError();
 }
 
-// Rows per CTA: the smallest of 8, 16, 32 that holds a sequence's rows of one
-// kv head, else tiles of 32. One resident wave: two CTAs per multiprocessor
-// with 8 rows, one with more (registers), and no more CTAs than rounds.
-tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int max_len, int sms, Kv4AttnPlan* pl) {
+// How a batch within these bounds runs. Sequences of up to 16 query rows per kv
+// head take this file's kernel, 8 rows per CTA if no sequence has more, else 16;
+// longer ones the prompt kernel, whose 128-row tiles cost the same tensor time
+// from 17 rows on as from 128 but no more than the codes' expansion.
+// Workspace: the CTAs' counters of both kernels, then their parts, at places that
+// only the device and the cache's shape decide, so that batches of any size share it.
+struct Plan {
+  int rows, ctas;           // few rows: rows per CTA, CTAs; 0 if the batch has none
+  int prompt_ctas;          // 0 if no sequence may have more than 16 rows
+  long long min_share;
+  size_t part_off, prompt_off, total;
+};
+constexpr int kMaxRows = 16;
+
+tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int max_len, int sms, Plan* pl) {
   const long long rows = (long long)max_new * (heads / c.kv_heads);
   if (rows > (1 << 30) || max_len > (1 << 30)) return TERN_EUNSUPPORTED;
-  pl->rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
-  const long long tiles = (rows + pl->rows - 1) / pl->rows, rounds = std::max(1, (max_len - 1) / kRound + 1);
-  // seqs x kv_heads x tiles x rounds must stay below 2^63 / kMaxCtas in the kernel
-  const double most = (double)seqs * c.kv_heads * (double)tiles * (double)rounds;
-  if (most > 1e15) return TERN_EUNSUPPORTED;
-  const int wave = std::min(kMaxCtas, (pl->rows == 8 ? 2 : 1) * sms);
-  pl->ctas = (int)std::min((double)wave, std::max(1.0, most));
-  // two slots per CTA of the largest wave, and a counter, at places that no batch changes
-  pl->cnt_bytes = kMaxCtas * sizeof(unsigned);
-  pl->ws_bytes = rounds > 1 ? pl->cnt_bytes + (size_t)wave * 2 * pl->rows * (size_t)(c.dim + 2) * 4 : 0;
+  const long long rounds = std::max(1, (max_len - 1) / kRound + 1), blocks = std::max(1, (max_len - 1) / 128 + 1);
+  // the kernels count rounds times CTAs in 64 bits
+  if ((double)seqs * c.kv_heads * (double)((rows + 7) / 8) * (double)blocks > 1e15) return TERN_EUNSUPPORTED;
+  pl->rows = rows <= 8 ? 8 : 16;
+  // one resident wave: two CTAs per multiprocessor with 8 rows, one with 16 (registers)
+  const int wave = std::min(kMaxCtas, (pl->rows == 8 ? 2 : 1) * sms), prompt_wave = std::min(kMaxCtas, sms);
+  pl->ctas = (int)std::min<double>(wave, std::max(1.0, (double)seqs * c.kv_heads * 2 * (double)rounds));
+  pl->prompt_ctas = 0;
+  if (rows > kMaxRows) {
+    pl->prompt_ctas = prompt_wave;
+    if (seqs == 1) pl->ctas = 0;  // the prompt kernel takes the one sequence whatever its length
+  }
+  // a CTA of the prompt kernel takes four blocks or more, and no unit is cut
+  // into more than about 16 parts, which its last CTA reads
+  pl->min_share = std::max(4ll, blocks / 16);
+  const size_t slot8 = (size_t)8 * (size_t)(c.dim + 2) * 4;
+  pl->part_off = 2 * kMaxCtas * sizeof(unsigned);
+  // 2 wave slots of 8 rows or wave slots of 16: the same size
+  pl->prompt_off = pl->part_off + ((size_t)std::min(kMaxCtas, 2 * sms) * 2 * slot8 + 255) / 256 * 256;
+  pl->total = pl->prompt_ctas ? pl->prompt_off + kv4_prompt_part_bytes(c.dim, prompt_wave)
+                              : (rounds > 1 ? pl->prompt_off : 0);
   return TERN_OK;
 }
 
 }  // namespace
 
-int launch_kv4_attn(const Kv4AttnParams& p, const Kv4AttnPlan& pl, void* stream) {
+int launch_kv4_attn(const Kv4AttnParams& p, int rows, int ctas, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int blocks = pl.ctas;
-  if (p.c.dim == 128) {
-    if (pl.rows == 8) return launch_one<128, 1>(p, blocks, s);
-    if (pl.rows == 16) return launch_one<128, 2>(p, blocks, s);
-    return launch_one<128, 4>(p, blocks, s);
-  }
-  if (pl.rows == 8) return launch_one<64, 1>(p, blocks, s);
-  if (pl.rows == 16) return launch_one<64, 2>(p, blocks, s);
-  return launch_one<64, 4>(p, blocks, s);
+  if (p.c.dim == 128) return rows == 8 ? launch_one<128, 1>(p, ctas, s) : launch_one<128, 2>(p, ctas, s);
+  return rows == 8 ? launch_one<64, 1>(p, ctas, s) : launch_one<64, 2>(p, ctas, s);
 }
 
 }  // namespace tern
@@ -704,10 +658,10 @@ extern "C" tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* c
   if (st != TERN_OK) return st;
   if (seqs < 0 || seqs > 65535 || max_new < 0 || max_len < 0 || heads < 1 || heads % c.kv_heads != 0)
     return TERN_EINVAL;
-  Kv4AttnPlan pl{};
+  Plan pl{};
   const tern_status sp = plan_attn(c, heads, seqs, max_new, max_len, sm_count(), &pl);
   if (sp != TERN_OK) return sp;
-  *bytes = seqs > 0 && max_new > 0 ? pl.ws_bytes : 0;
+  *bytes = seqs > 0 && max_new > 0 ? pl.total : 0;
   return TERN_OK;
 }
 
@@ -722,19 +676,35 @@ extern "C" tern_status tern_kv4_attention(const tern_kv4_cache* cache, const ter
   if (p.c.seqs == 0 || p.c.tokens == 0 || p.c.max_new == 0) return TERN_OK;
   if (!d_q || !d_out) return TERN_EINVAL;
   if (((reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_out)) & 15u) != 0) return TERN_EALIGN;
-  Kv4AttnPlan pl{};
+  Plan pl{};
   st = plan_attn(p.c, heads, p.c.seqs, p.c.max_new, p.c.max_len, sm_count(), &pl);
   if (st != TERN_OK) return st;
-  if (pl.ws_bytes > 0) {
-    if (!d_ws || ws_bytes < pl.ws_bytes) return TERN_ENOSPACE;
+  if (pl.total > 0) {
+    if (!d_ws || ws_bytes < pl.total) return TERN_ENOSPACE;
     if ((reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0) return TERN_EALIGN;
   }
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
   p.c.heads = heads;
   p.q = d_q;
   p.out = d_out;
   p.scale_log2 = scale * 1.44269504088896340736f;
   p.group = heads / p.c.kv_heads;
-  p.cnt = static_cast<unsigned*>(d_ws);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + pl.cnt_bytes);
-  return launch_kv4_attn(p, pl, stream) == 0 ? TERN_OK : TERN_ECUDA;
+  p.max_rows = kMaxRows;
+  p.cnt = reinterpret_cast<unsigned*>(ws);
+  p.part = reinterpret_cast<float*>(ws + pl.part_off);
+  if (pl.prompt_ctas) {
+    Kv4PromptParams r{};
+    r.c = p.c;
+    r.q = p.q;
+    r.out = p.out;
+    r.scale_log2 = p.scale_log2;
+    r.group = p.group;
+    r.min_rows = pl.ctas ? kMaxRows + 1 : 1;
+    r.min_share = pl.min_share;
+    r.cnt = p.cnt + kMaxCtas;
+    r.part = reinterpret_cast<float*>(ws + pl.prompt_off);
+    if (launch_kv4_prompt(r, pl.prompt_ctas, stream) != 0) return TERN_ECUDA;
+  }
+  if (pl.ctas && launch_kv4_attn(p, pl.rows, pl.ctas, stream) != 0) return TERN_ECUDA;
+  return TERN_OK;
 }
