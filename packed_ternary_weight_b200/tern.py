@@ -283,39 +283,54 @@ def fit_bt(w, depth: int, codebook, trits, idx, stream=None):
            "tern_fit_bt")
 
 
+_torch = None
+
+
+def _import_torch():
+    """torch, imported on first use (packing needs none); its types as TERN_OUT_*."""
+    global _torch, _OUT_TYPE
+    import torch
+    _OUT_TYPE = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    _torch = torch
+    return torch
+
+
+def _bad(what: str):
+    raise TernError(EINVAL, what)
+
+
 def _type(t, what: str) -> int:
     """TERN_OUT_* of a float tensor."""
-    name = str(t.dtype)
-    if name == "torch.float32":
-        return OUT_F32
-    if name == "torch.bfloat16":
-        return OUT_BF16
-    raise TernError(EINVAL, f"{what}: {name} is neither float32 nor bfloat16")
-
-
-def _want(ok: bool, what: str):
-    if not ok:
-        raise TernError(EINVAL, what)
+    o = _OUT_TYPE.get(t.dtype)
+    return o if o is not None else _bad(f"{what}: {t.dtype} is neither float32 nor bfloat16")
 
 
 def _rows(t, m: int, k: int, what: str) -> int:
     """Row stride of a tensor [m][k] whose rows are contiguous."""
-    _want(t.dim() == 2 and t.shape[0] == m and t.shape[1] == k and (k == 1 or t.stride(1) == 1), what)
-    return t.stride(0) if m > 1 else max(k, t.stride(0))
+    if t.dim() != 2 or tuple(t.shape) != (m, k):
+        _bad(what)
+    ld, one = t.stride()
+    if one != 1 and k > 1:
+        _bad(what)
+    return ld if m > 1 and ld > k else k if m <= 1 else ld
 
 
-def _vector(t, n: int, name: str, what: str):
-    _want(str(t.dtype) == name and t.numel() == n and t.is_contiguous(), what)
+def _vector(t, n: int, dtype, what: str):
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _bad(what)
 
 
-def _launch(dev, stream, what: str, fn, *args):
-    """Call an entry point on the device that the tensors are on."""
-    import torch
-    _want(dev.type == "cuda", f"{what}: tensors are not on a CUDA device")
-    if dev.index == torch.cuda.current_device():
-        return _check(fn(*args, _stream(stream)), what)
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream(stream)), what)
+def _launch(dev: int, stream, what: str, fn, *args):
+    """Call an entry point on the device that the tensors are on (their get_device())."""
+    if dev < 0:
+        _bad(f"{what}: tensors are not on a CUDA device")
+    cuda = _torch.cuda
+    if dev != cuda.current_device():
+        with cuda.device(dev):
+            return _launch(dev, stream, what, fn, *args)
+    code = fn(*args, cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+    if code != OK:
+        raise TernError(code, what)
 
 
 def norm_quantize(mode: int, x, r, gain, eps: float, sum, xq, xscale, stream=None):
@@ -323,42 +338,54 @@ def norm_quantize(mode: int, x, r, gain, eps: float, sum, xq, xscale, stream=Non
     to int8 per row: x, r, sum [m][k] float32 or bfloat16 (sum of r's type, or r itself), gain float32 [k], xq int8
     [m][k], xscale float32 [m]."""
     what = "tern_norm_quantize"
+    t = _torch or _import_torch()
     m, k = x.shape
-    two, add = mode != NORM_PLAIN, mode == NORM_ADD
-    _want(not two or r is not None, f"{what}: r is missing")
-    _want(not add or (sum is not None and sum.dtype == r.dtype), f"{what}: sum has r's type")
-    _vector(gain, k, "torch.float32", f"{what}: gain")
-    _vector(xscale, m, "torch.float32", f"{what}: xscale")
-    _want(str(xq.dtype) == "torch.int8", f"{what}: xq is int8")
-    dev = x.device
-    _want(gain.device == dev and xq.device == dev and xscale.device == dev and (not two or r.device == dev) and
-          (not add or sum.device == dev), f"{what}: tensors on several devices")
+    dev = x.get_device()
+    _vector(gain, k, t.float32, "tern_norm_quantize: gain")
+    _vector(xscale, m, t.float32, "tern_norm_quantize: xscale")
+    if xq.dtype is not t.int8:
+        _bad(f"{what}: xq is int8")
+    rt, rp, ldr, sp, lds = 0, None, 0, None, 0
+    if mode != NORM_PLAIN:
+        if r is None:
+            _bad(f"{what}: r is missing")
+        rt, rp, ldr = _type(r, what), r.data_ptr(), _rows(r, m, k, "tern_norm_quantize: r")
+        if r.get_device() != dev:
+            _bad(f"{what}: tensors on several devices")
+    if mode == NORM_ADD:
+        if sum is None or sum.dtype is not r.dtype:
+            _bad(f"{what}: sum has r's type")
+        sp, lds = sum.data_ptr(), _rows(sum, m, k, "tern_norm_quantize: sum")
+        if sum.get_device() != dev:
+            _bad(f"{what}: tensors on several devices")
+    if gain.get_device() != dev or xq.get_device() != dev or xscale.get_device() != dev:
+        _bad(f"{what}: tensors on several devices")
     _launch(dev, stream, what, lib.tern_norm_quantize, mode, m, k, _type(x, what), x.data_ptr(),
-            _rows(x, m, k, f"{what}: x"), _type(r, what) if two else 0, r.data_ptr() if two else None,
-            _rows(r, m, k, f"{what}: r") if two else 0, gain.data_ptr(), eps, sum.data_ptr() if add else None,
-            _rows(sum, m, k, f"{what}: sum") if add else 0, xq.data_ptr(), _rows(xq, m, k, f"{what}: xq"),
-            xscale.data_ptr())
+            _rows(x, m, k, "tern_norm_quantize: x"), rt, rp, ldr, gain.data_ptr(), eps, sp, lds, xq.data_ptr(),
+            _rows(xq, m, k, "tern_norm_quantize: xq"), xscale.data_ptr())
 
 
 def gemm_i8(x, xscale, w, wscale, y, stream=None):
     """y[m][n] = x[m][k] w[n][k]^T with a scale per row of x and of w: x, w int8 (row strides multiples of 16), xscale
     float32 [m], wscale float32 [n], y float32 or bfloat16."""
     what = "tern_gemm_i8"
+    t = _torch or _import_torch()
     m, k = x.shape
     n = w.shape[0]
-    _want(str(x.dtype) == "torch.int8" and str(w.dtype) == "torch.int8", f"{what}: x and w are int8")
-    _vector(xscale, m, "torch.float32", f"{what}: xscale")
-    _vector(wscale, n, "torch.float32", f"{what}: wscale")
-    dev = x.device
-    _want(w.device == dev and xscale.device == dev and wscale.device == dev and y.device == dev,
-          f"{what}: tensors on several devices")
-    ldx, ldw = _rows(x, m, k, f"{what}: x"), _rows(w, n, k, f"{what}: w")
+    if x.dtype is not t.int8 or w.dtype is not t.int8:
+        _bad(f"{what}: x and w are int8")
+    _vector(xscale, m, t.float32, "tern_gemm_i8: xscale")
+    _vector(wscale, n, t.float32, "tern_gemm_i8: wscale")
+    dev = x.get_device()
+    if w.get_device() != dev or xscale.get_device() != dev or wscale.get_device() != dev or y.get_device() != dev:
+        _bad(f"{what}: tensors on several devices")
+    ldx, ldw = _rows(x, m, k, "tern_gemm_i8: x"), _rows(w, n, k, "tern_gemm_i8: w")
     if m <= 1:
         ldx = (ldx + 15) & ~15  # the stride of a single row is free
     if n <= 1:
         ldw = (ldw + 15) & ~15
     _launch(dev, stream, what, lib.tern_gemm_i8, m, n, k, x.data_ptr(), ldx, xscale.data_ptr(), w.data_ptr(), ldw,
-            wscale.data_ptr(), _type(y, what), y.data_ptr(), _rows(y, m, n, f"{what}: y"))
+            wscale.data_ptr(), _type(y, what), y.data_ptr(), _rows(y, m, n, "tern_gemm_i8: y"))
 
 
 class KV4Batch:
@@ -367,16 +394,20 @@ class KV4Batch:
 
     def __init__(self, start, len, table, tokens: int, max_new: int, max_len: int):
         what = "tern_kv4_batch"
+        i32 = (_torch or _import_torch()).int32
         seqs = start.numel() - 1
-        _vector(start, seqs + 1, "torch.int32", f"{what}: start")
-        _vector(len, seqs, "torch.int32", f"{what}: len")
-        _want(table.dim() == 2 and table.shape[0] == seqs, f"{what}: table")
-        _vector(table, table.numel(), "torch.int32", f"{what}: table")
-        _want(len.device == start.device and table.device == start.device, f"{what}: tensors on several devices")
+        _vector(start, seqs + 1, i32, "tern_kv4_batch: start")
+        _vector(len, seqs, i32, "tern_kv4_batch: len")
+        if table.dim() != 2 or table.shape[0] != seqs or table.dtype is not i32 or not table.is_contiguous():
+            _bad(f"{what}: table")
+        self.dev = start.get_device()
+        if len.get_device() != self.dev or table.get_device() != self.dev:
+            _bad(f"{what}: tensors on several devices")
         self._keep = (start, len, table)
-        self.device, self.tokens = start.device, tokens
+        self.tokens = tokens
         self.c = KV4BatchC(seqs, tokens, max_new, max_len, table.shape[1], start.data_ptr(), len.data_ptr(),
                            table.data_ptr())
+        self._ref = ctypes.byref(self.c)
 
 
 class KV4Cache:
@@ -384,10 +415,12 @@ class KV4Cache:
 
     def __init__(self, pages, kv_heads: int, head_dim: int, page_size: int):
         what = "tern_kv4_cache"
-        _want(str(pages.dtype) == "torch.uint8" and pages.is_contiguous(), f"{what}: pages is contiguous uint8")
         page_bytes = kv_heads * page_size * (head_dim + 8)
-        _want(page_bytes > 0 and pages.numel() % page_bytes == 0, f"{what}: pages holds whole pages")
-        self._keep, self.device = pages, pages.device
+        if pages.dtype is not (_torch or _import_torch()).uint8 or not pages.is_contiguous():
+            _bad(f"{what}: pages is contiguous uint8")
+        if page_bytes <= 0 or pages.numel() % page_bytes:
+            _bad(f"{what}: pages holds whole pages")
+        self._keep, self.dev = pages, pages.get_device()
         self.kv_heads, self.head_dim = kv_heads, head_dim
         self.c = KV4CacheC(kv_heads, head_dim, page_size, pages.numel() // page_bytes, pages.data_ptr())
         self._ref = ctypes.byref(self.c)
@@ -400,45 +433,51 @@ class KV4Cache:
         _check(lib.tern_kv4_cache_size(ctypes.byref(c), ctypes.byref(out)), "tern_kv4_cache_size")
         return out.value
 
-    def _heads(self, t, tokens: int, what: str):
-        """Heads and row stride of a token buffer [tokens][heads * head_dim]."""
-        _want(t.device == self.device, f"{what}: tensors on several devices")
-        _want(t.dim() == 2 and t.shape[1] % self.head_dim == 0, what)
-        return t.shape[1] // self.head_dim, _rows(t, tokens, t.shape[1], what)
+    def _width(self, t, tokens: int, heads: int, what: str) -> int:
+        """Row stride of a token buffer [tokens][heads * head_dim] on the cache's device."""
+        if t.get_device() != self.dev:
+            _bad(f"{what}: tensors on several devices")
+        return _rows(t, tokens, heads * self.head_dim, what)
 
     def append(self, batch: KV4Batch, q, k, v, rope, q_out, stream=None):
         """Rotate q and k by position, store k and v. q [tokens][heads * head_dim] and q_out (bfloat16, contiguous)
         may both be None; q, k, v are float32 or bfloat16, rope is the float32 table of decode_rope_table."""
         what = "tern_kv4_append"
-        n = batch.tokens
-        heads, ldq = (0, 0) if q is None else self._heads(q, n, f"{what}: q")
-        hk, ldk = self._heads(k, n, f"{what}: k")
-        hv, ldv = self._heads(v, n, f"{what}: v")
-        _want(hk == self.kv_heads and hv == hk, f"{what}: k and v have the cache's heads")
-        _want(v.dtype == k.dtype and (q is None or q.dtype == k.dtype), f"{what}: q, k and v have one type")
+        n, d = batch.tokens, self.head_dim
+        heads, ldq, qp, qo = 0, 0, None, None
         if q is not None:
-            _want(q_out is not None and q_out.device == self.device, f"{what}: q_out")
-            _vector(q_out, n * heads * self.head_dim, "torch.bfloat16", f"{what}: q_out")
-        _want(rope.dim() == 3 and rope.shape[1] * 2 == self.head_dim and rope.shape[2] == 2 and
-              rope.device == self.device and batch.device == self.device, f"{what}: rope")
-        _vector(rope, rope.numel(), "torch.float32", f"{what}: rope")
-        _launch(self.device, stream, what, lib.tern_kv4_append, self._ref, ctypes.byref(batch.c), heads,
-                _type(k, what), None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                rope.data_ptr(), rope.shape[0], None if q is None else q_out.data_ptr())
+            heads = q.shape[-1] // d
+            ldq, qp = self._width(q, n, heads, "tern_kv4_append: q"), q.data_ptr()
+            if q_out is None or q_out.get_device() != self.dev:
+                _bad(f"{what}: q_out")
+            _vector(q_out, n * heads * d, _torch.bfloat16, "tern_kv4_append: q_out")
+            qo = q_out.data_ptr()
+        ldk = self._width(k, n, self.kv_heads, "tern_kv4_append: k")
+        ldv = self._width(v, n, self.kv_heads, "tern_kv4_append: v")
+        if v.dtype is not k.dtype or (q is not None and q.dtype is not k.dtype):
+            _bad(f"{what}: q, k and v have one type")
+        max_pos = rope.shape[0]
+        _vector(rope, max_pos * d, _torch.float32, "tern_kv4_append: rope")
+        if rope.get_device() != self.dev or batch.dev != self.dev:
+            _bad(f"{what}: tensors on several devices")
+        _launch(self.dev, stream, what, lib.tern_kv4_append, self._ref, batch._ref, heads, _type(k, what), qp, ldq,
+                k.data_ptr(), ldk, v.data_ptr(), ldv, rope.data_ptr(), max_pos, qo)
 
     def read(self, batch: KV4Batch, k, v, stream=None):
         """The cached keys and values of the batch's tokens into k and v [tokens][kv_heads * head_dim] (one may be
         None), float32 or bfloat16."""
         what = "tern_kv4_read"
-        _want(k is not None or v is not None, f"{what}: neither k nor v")
-        hk, ldk = (self.kv_heads, 0) if k is None else self._heads(k, batch.tokens, f"{what}: k")
-        hv, ldv = (self.kv_heads, 0) if v is None else self._heads(v, batch.tokens, f"{what}: v")
-        _want(hk == self.kv_heads and hv == hk, f"{what}: k and v have the cache's heads")
-        _want(k is None or v is None or k.dtype == v.dtype, f"{what}: k and v have one type")
-        _want(batch.device == self.device, f"{what}: tensors on several devices")
-        _launch(self.device, stream, what, lib.tern_kv4_read, self._ref, ctypes.byref(batch.c),
-                _type(v if k is None else k, what), None if k is None else k.data_ptr(), ldk,
-                None if v is None else v.data_ptr(), ldv)
+        one = v if k is None else k
+        if one is None:
+            _bad(f"{what}: neither k nor v")
+        ldk = 0 if k is None else self._width(k, batch.tokens, self.kv_heads, "tern_kv4_read: k")
+        ldv = 0 if v is None else self._width(v, batch.tokens, self.kv_heads, "tern_kv4_read: v")
+        if v is not None and v.dtype is not one.dtype:
+            _bad(f"{what}: k and v have one type")
+        if batch.dev != self.dev:
+            _bad(f"{what}: tensors on several devices")
+        _launch(self.dev, stream, what, lib.tern_kv4_read, self._ref, batch._ref, _type(one, what),
+                None if k is None else k.data_ptr(), ldk, None if v is None else v.data_ptr(), ldv)
 
     def attention_workspace_size(self, seqs: int, max_new: int, max_len: int, heads: int) -> int:
         out = _sz()
@@ -450,12 +489,12 @@ class KV4Cache:
         """Causal attention of the batch's new tokens over the cache: q, out bfloat16 [tokens][heads * head_dim]
         contiguous (out may be q); ws uint8, zero before its first use (attention_workspace_size)."""
         what = "tern_kv4_attention"
-        _want(q.dim() == 2 and q.shape[1] % self.head_dim == 0 and batch.device == self.device and
-              q.device == self.device and out.device == self.device and (ws is None or ws.device == self.device),
-              f"{what}: q")
-        heads = q.shape[1] // self.head_dim
-        _vector(q, batch.tokens * q.shape[1], "torch.bfloat16", f"{what}: q")
-        _vector(out, q.numel(), "torch.bfloat16", f"{what}: out")
-        _launch(self.device, stream, what, lib.tern_kv4_attention, self._ref, ctypes.byref(batch.c), heads, scale,
-                q.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(),
-                0 if ws is None else ws.numel() * ws.element_size())
+        width, dev = q.shape[-1], self.dev
+        heads = width // self.head_dim
+        bf16 = _torch.bfloat16
+        _vector(q, batch.tokens * heads * self.head_dim, bf16, "tern_kv4_attention: q")
+        _vector(out, batch.tokens * width, bf16, "tern_kv4_attention: out")
+        if batch.dev != dev or q.get_device() != dev or out.get_device() != dev or (ws is not None and ws.get_device() != dev):
+            _bad(f"{what}: tensors on several devices")
+        _launch(dev, stream, what, lib.tern_kv4_attention, self._ref, batch._ref, heads, scale, q.data_ptr(),
+                out.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
