@@ -433,7 +433,7 @@ typedef struct tern_kv4_cache {
  * The new tokens of a step: sequence s has the rows d_start[s] .. d_start[s+1]-1
  * of the token buffers and, with them, d_len[s] tokens in all, so its i-th new
  * token is at position d_len[s] - (number of new tokens) + i. Rows from
- * d_start[seqs] on belong to no sequence: no call reads or writes them.
+ * d_start[seqs] on belong to no sequence: no call uses or writes them.
  * A new token whose position is negative is not stored, its query is zero and
  * its attention output is zero. The lengths and the table are read by the
  * kernels, so a captured launch follows what they hold when it is replayed; a

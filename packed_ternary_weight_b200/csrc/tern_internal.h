@@ -337,8 +337,9 @@ struct Kv4AppendParams {
   uint16_t* q_out;
   int64_t ldq, ldk, ldv;
   int max_pos, bf16;
+  int warps_per_token;  // set at launch
 };
-int launch_kv4_append(const Kv4AppendParams& p, void* stream);
+int launch_kv4_append(Kv4AppendParams p, void* stream);
 
 struct Kv4ReadParams {
   Kv4Params c;
@@ -346,8 +347,9 @@ struct Kv4ReadParams {
   void* v;
   int64_t ldk, ldv;
   int bf16;
+  int warps_per_token;  // set at launch
 };
-int launch_kv4_read(const Kv4ReadParams& p, void* stream);
+int launch_kv4_read(Kv4ReadParams p, void* stream);
 int read_clear_dev_error_kv4(void* stream, unsigned* out);
 
 // Attention over few query rows per sequence and kv head (up to max_rows; others

@@ -3,11 +3,13 @@
 // with one fp16 (scale, min) pair: 4.25 bits per value at D = 128, against 16
 // of the decode step's bf16 cache.
 //
-// One group of D / 4 lanes takes one (token, head): lane l holds the
-// dimensions 2l, 2l+1 and D/2 + 2l, D/2 + 2l + 1, the two pairs that
-// rotate_half combines, so the rotation needs no exchange and each lane's two
-// code pairs are two whole bytes. Minimum and maximum go over the group by
-// shuffles.
+// A group of D / 8 lanes takes one (token, head) at a time: lane l holds the
+// dimensions 4l .. 4l + 3 and D/2 + 4l .. + 3, the pairs that rotate_half combines,
+// so the rotation needs no exchange and each lane's codes are two pairs of whole
+// bytes. Minimum and maximum go over the group by shuffles. A warp takes one
+// head per group of a few tokens and up to six of each of many: the search for
+// the token's sequence, its rotation row and its page are then shared by them,
+// and the heads' loads are issued together, ahead of that search.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,27 +40,69 @@ __device__ __forceinline__ int seq_of(const Kv4Params& c, int t) {
   return lo < c.seqs ? lo : -1;
 }
 
-__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+// Four elements as they stand in memory.
+template <typename T>
+struct Raw4 {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float (&v)[4]) const {
+    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+  }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void values(float (&v)[4]) const {
+    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  }
+};
+__device__ __forceinline__ void st4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void st2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
-__device__ __forceinline__ void st2(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <int D, typename T>
+constexpr int kMaxHeads = 6;  // of a token that a group of lanes takes
+
+// A warp's token and the heads of its groups: first, first + step, .. (count of them, the same in both groups).
+template <int D>
+struct Place {
+  static constexpr int L = D / 8, kGroups = 32 / L;
+  int t, first, step, gl;
+  __device__ __forceinline__ bool find(const Kv4Params& c, int warps_per_token) {
+    const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const long long tl = w / warps_per_token;
+    if (tl >= c.tokens) return false;  // whole warps
+    t = (int)tl;
+    gl = threadIdx.x & (L - 1);
+    first = (int)(w - tl * warps_per_token) * kGroups + (int)((threadIdx.x & 31) / L);
+    step = warps_per_token * kGroups;
+    return true;
+  }
+};
+
+template <int D, typename T, int HEADS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams p) {
-  constexpr int L = D / 4;  // lanes of a group
   const Kv4Params& c = p.c;
-  const int groups = c.heads + 2 * c.kv_heads;  // of a token: q heads, k heads, v heads
-  const int gl = threadIdx.x & (L - 1);
-  // a warp's groups are of one token: groups rounded up to whole warps
-  const int wpt = (groups * L + 31) >> 5;  // warps per token
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long tl = w / wpt;
-  if (tl >= c.tokens) return;  // whole warps
-  const int t = (int)tl;
+  const int total = c.heads + 2 * c.kv_heads;  // of a token: q heads, k heads, v heads
+  Place<D> pl;
+  if (!pl.find(c, p.warps_per_token)) return;
+  const int t = pl.t, gl = pl.gl;
+  Raw4<T> lo[HEADS], hi[HEADS];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int g = min(pl.first + i * pl.step, total - 1);
+    const T* src = g < c.heads ? static_cast<const T*>(p.q) + (int64_t)t * p.ldq + (size_t)g * D
+                   : g < c.heads + c.kv_heads
+                       ? static_cast<const T*>(p.k) + (int64_t)t * p.ldk + (size_t)(g - c.heads) * D
+                       : static_cast<const T*>(p.v) + (int64_t)t * p.ldv + (size_t)(g - c.heads - c.kv_heads) * D;
+    lo[i].load(src + 4 * gl);
+    hi[i].load(src + D / 2 + 4 * gl);
+  }
   const int s = seq_of(c, t);
   if (s < 0) return;
   const kv4::Seq q = kv4::load_seq(c, s);
@@ -66,79 +110,81 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
     kv4::report_bad();
     return;
   }
-  const int g = (int)(w - tl * wpt) * (32 / L) + (int)((threadIdx.x & 31) / L);
-  const bool active = g < groups;
   const int pos = q.len - q.n + (t - q.row0);
-  const bool is_q = g < c.heads, is_k = !is_q && g < c.heads + c.kv_heads;
-  const int head = is_q ? g : (is_k ? g - c.heads : g - c.heads - c.kv_heads);
-  __nv_bfloat16* qo = reinterpret_cast<__nv_bfloat16*>(p.q_out) + ((size_t)t * c.heads + head) * D + 2 * gl;
-  if (pos < 0 || pos >= p.max_pos) {
-    if (pos >= 0) kv4::report_bad();
-    if (active && is_q) {
-      st2(qo, 0.f, 0.f);
-      st2(qo + D / 2, 0.f, 0.f);
-    }
-    return;
+  const bool skip = pos < 0 || pos >= p.max_pos;  // not stored, its query is zero
+  if (pos >= p.max_pos) kv4::report_bad();
+  int page = -1;
+  float4 cs0 = make_float4(0.f, 0.f, 0.f, 0.f), cs1 = cs0;
+  if (!skip) {
+    page = kv4::page_of(c, s, pos);
+    if (page < 0) kv4::report_bad();
+    const float4* row = reinterpret_cast<const float4*>(p.rope + ((size_t)pos * (D / 2) + 4 * gl) * 2);
+    cs0 = __ldg(row);
+    cs1 = __ldg(row + 1);
   }
-  const T* src = is_q ? static_cast<const T*>(p.q) + (int64_t)t * p.ldq
-                      : (is_k ? static_cast<const T*>(p.k) + (int64_t)t * p.ldk
-                              : static_cast<const T*>(p.v) + (int64_t)t * p.ldv);
-  float2 a = make_float2(0.f, 0.f), b = a;
-  if (active) {
-    a = ld2(src + (size_t)head * D + 2 * gl);
-    b = ld2(src + (size_t)head * D + D / 2 + 2 * gl);
-    if (is_q || is_k) {
-      const float4 cs = __ldg(reinterpret_cast<const float4*>(p.rope + ((size_t)pos * (D / 2) + 2 * gl) * 2));
-      const float2 x = a, y = b;
-      a.x = __fsub_rn(__fmul_rn(x.x, cs.x), __fmul_rn(y.x, cs.y));
-      b.x = __fadd_rn(__fmul_rn(y.x, cs.x), __fmul_rn(x.x, cs.y));
-      a.y = __fsub_rn(__fmul_rn(x.y, cs.z), __fmul_rn(y.y, cs.w));
-      b.y = __fadd_rn(__fmul_rn(y.y, cs.z), __fmul_rn(x.y, cs.w));
-    }
-  }
-  float lo = fminf(fminf(a.x, a.y), fminf(b.x, b.y)), hi = fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
+  const float co[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, si[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
 #pragma unroll
-  for (int o = L / 2; o; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  for (int i = 0; i < HEADS; ++i) {
+    const int g = pl.first + i * pl.step;
+    const bool is_q = g < c.heads, is_k = !is_q && g < c.heads + c.kv_heads;
+    float a[4], b[4];
+    lo[i].values(a);
+    hi[i].values(b);
+    if (is_q || is_k) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = a[k], y = b[k];
+        a[k] = __fsub_rn(__fmul_rn(x, co[k]), __fmul_rn(y, si[k]));
+        b[k] = __fadd_rn(__fmul_rn(y, co[k]), __fmul_rn(x, si[k]));
+      }
+    }
+    if (is_q) {
+      __nv_bfloat16* qo = reinterpret_cast<__nv_bfloat16*>(p.q_out) + ((size_t)t * c.heads + g) * D + 4 * gl;
+      if (skip) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = b[k] = 0.f;
+      }
+      st4(qo, a);
+      st4(qo + D / 2, b);
+    }
+    // a warp whose groups all hold queries skips the rest
+    if (__all_sync(0xffffffffu, is_q || g >= total)) continue;
+    float mn = fminf(fminf(fminf(a[0], a[1]), fminf(a[2], a[3])), fminf(fminf(b[0], b[1]), fminf(b[2], b[3])));
+    float mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
+#pragma unroll
+    for (int o = Place<D>::L / 2; o; o >>= 1) {
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if (is_q || g >= total || page < 0) continue;
+    const int head = is_k ? g - c.heads : g - c.heads - c.kv_heads;
+    const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f)), hm = __float2half_rn(mn);
+    const float sc = __half2float(hs), m = __half2float(hm);
+    const float inv = sc > 0.f ? __fdiv_rn(1.0f, sc) : 0.f;
+    auto code = [&](float v) {
+      return (unsigned)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(v, m), inv))));
+    };
+    auto four = [&](const float (&v)[4]) {
+      return (uint16_t)(code(v[0]) | (code(v[1]) << 4) | (code(v[2]) << 8) | (code(v[3]) << 12));
+    };
+    uint8_t* blk = c.pages + kv4::block_offset(c, page, head);
+    const int slot = pos & (c.page - 1);
+    uint16_t* row = reinterpret_cast<uint16_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
+    row[gl] = four(a);
+    row[D / 8 + gl] = four(b);
+    if (gl == 0)
+      *reinterpret_cast<__half2*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4)) =
+          __halves2half2(hs, hm);
   }
-  if (!active) return;
-  if (is_q) {
-    st2(qo, a.x, a.y);
-    st2(qo + D / 2, b.x, b.y);
-    return;
-  }
-  const int page = kv4::page_of(c, s, pos);
-  if (page < 0) {
-    kv4::report_bad();
-    return;
-  }
-  const __half hs = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), hm = __float2half_rn(lo);
-  const float sc = __half2float(hs), mn = __half2float(hm);
-  const float inv = sc > 0.f ? __fdiv_rn(1.0f, sc) : 0.f;
-  auto code = [&](float v) {
-    return (unsigned)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(v, mn), inv))));
-  };
-  uint8_t* blk = c.pages + kv4::block_offset(c, page, head);
-  const int slot = pos & (c.page - 1);
-  uint8_t* row = blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2);
-  row[gl] = (uint8_t)(code(a.x) | (code(a.y) << 4));
-  row[D / 4 + gl] = (uint8_t)(code(b.x) | (code(b.y) << 4));
-  if (gl == 0)
-    *reinterpret_cast<__half2*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4)) = __halves2half2(hs, hm);
 }
 
-template <int D, typename T>
+template <int D, typename T, int HEADS>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
-  constexpr int L = D / 4;
   const Kv4Params& c = p.c;
-  const int groups = 2 * c.kv_heads;
-  const int gl = threadIdx.x & (L - 1);
-  const int wpt = (groups * L + 31) >> 5;
-  const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long tl = w / wpt;
-  if (tl >= c.tokens) return;
-  const int t = (int)tl;
+  const int total = 2 * c.kv_heads;
+  Place<D> pl;
+  if (!pl.find(c, p.warps_per_token)) return;
+  const int t = pl.t, gl = pl.gl;
   const int s = seq_of(c, t);
   if (s < 0) return;
   const kv4::Seq q = kv4::load_seq(c, s);
@@ -146,65 +192,97 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
     kv4::report_bad();
     return;
   }
-  const int g = (int)(w - tl * wpt) * (32 / L) + (int)((threadIdx.x & 31) / L);
-  if (g >= groups) return;
-  const bool is_k = g < c.kv_heads;
-  const int head = is_k ? g : g - c.kv_heads;
-  void* dst = is_k ? p.k : p.v;
-  if (!dst) return;
-  T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)head * D + 2 * gl;
   const int pos = q.len - q.n + (t - q.row0);
   const int page = pos < 0 ? -1 : kv4::page_of(c, s, pos);
-  if (page < 0) {
-    if (pos >= 0) kv4::report_bad();
-    st2(out, 0.f, 0.f);
-    st2(out + D / 2, 0.f, 0.f);
-    return;
-  }
-  const uint8_t* blk = c.pages + kv4::block_offset(c, page, head);
+  if (page < 0 && pos >= 0) kv4::report_bad();
   const int slot = pos & (c.page - 1);
-  const uint8_t* row = blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2);
-  const float2 sm = __half22float2(
-      *reinterpret_cast<const __half2*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4)));
-  // scale * code is exact in fp32 (11 + 4 bits), so the fused form rounds once, as the definition
-  auto val = [&](unsigned code) { return __fmaf_rn(sm.x, (float)code, sm.y); };
-  const unsigned u = row[gl], v = row[D / 4 + gl];
-  st2(out, val(u & 15u), val(u >> 4));
-  st2(out + D / 2, val(v & 15u), val(v >> 4));
+  uint32_t u[HEADS], v[HEADS], pair[HEADS];
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int g = min(pl.first + i * pl.step, total - 1);
+    const bool is_k = g < c.kv_heads;
+    u[i] = v[i] = pair[i] = 0u;
+    if (page >= 0) {
+      const uint8_t* blk = c.pages + kv4::block_offset(c, page, is_k ? g : g - c.kv_heads);
+      const uint16_t* row =
+          reinterpret_cast<const uint16_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
+      u[i] = row[gl];
+      v[i] = row[D / 8 + gl];
+      pair[i] = *reinterpret_cast<const uint32_t*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int g = pl.first + i * pl.step;
+    if (g >= total) break;
+    const bool is_k = g < c.kv_heads;
+    void* dst = is_k ? p.k : p.v;
+    if (!dst) continue;
+    const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pair[i]));
+    T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)(is_k ? g : g - c.kv_heads) * D + 4 * gl;
+    // scale * code is exact in fp32 (11 + 4 bits), so the fused form rounds once, as the definition
+    float a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = page < 0 ? 0.f : __fmaf_rn(sm.x, (float)((u[i] >> (4 * k)) & 15u), sm.y);
+      b[k] = page < 0 ? 0.f : __fmaf_rn(sm.x, (float)((v[i] >> (4 * k)) & 15u), sm.y);
+    }
+    st4(out, a);
+    st4(out + D / 2, b);
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-long long blocks_for(const Kv4Params& c, int groups) {
-  const long long warps = (long long)c.tokens * ((groups * (c.dim / 4) + 31) / 32);
-  return (warps + kThreads / 32 - 1) / (kThreads / 32);
+// Heads per group of lanes: as many as leave about 24 warps per multiprocessor,
+// and the warps of a token.
+struct Spread {
+  int heads, warps_per_token;
+  long long blocks;
+};
+Spread spread(const Kv4Params& c, int total) {
+  const int groups = 32 / (c.dim / 8);
+  const long long warps = (long long)c.tokens * ((total + groups - 1) / groups);  // with one head each
+  const long long many = warps / (24ll * sm_count());
+  Spread s;
+  s.heads = many >= kMaxHeads ? kMaxHeads : (many >= 3 ? 3 : 1);
+  s.warps_per_token = (total + s.heads * groups - 1) / (s.heads * groups);
+  s.blocks = ((long long)c.tokens * s.warps_per_token + kThreads / 32 - 1) / (kThreads / 32);
+  return s;
+}
+
+template <int D, typename T>
+void append_any(const Kv4AppendParams& p, const Spread& sp, cudaStream_t s) {
+  const unsigned grid = (unsigned)sp.blocks;
+  if (sp.heads == kMaxHeads) append_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
+  else if (sp.heads == 3) append_kernel<D, T, 3><<<grid, kThreads, 0, s>>>(p);
+  else append_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
+}
+template <int D, typename T>
+void read_any(const Kv4ReadParams& p, const Spread& sp, cudaStream_t s) {
+  const unsigned grid = (unsigned)sp.blocks;
+  if (sp.heads == kMaxHeads) read_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
+  else if (sp.heads == 3) read_kernel<D, T, 3><<<grid, kThreads, 0, s>>>(p);
+  else read_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
 }
 
 }  // namespace
 
-int launch_kv4_append(const Kv4AppendParams& p, void* stream) {
-  const unsigned grid = (unsigned)blocks_for(p.c, p.c.heads + 2 * p.c.kv_heads);
+int launch_kv4_append(Kv4AppendParams p, void* stream) {
+  const Spread sp = spread(p.c, p.c.heads + 2 * p.c.kv_heads);
+  p.warps_per_token = sp.warps_per_token;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.c.dim == 128) {
-    if (p.bf16) append_kernel<128, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else append_kernel<128, float><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (p.bf16) append_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else append_kernel<64, float><<<grid, kThreads, 0, s>>>(p);
-  }
+  if (p.c.dim == 128) p.bf16 ? append_any<128, __nv_bfloat16>(p, sp, s) : append_any<128, float>(p, sp, s);
+  else p.bf16 ? append_any<64, __nv_bfloat16>(p, sp, s) : append_any<64, float>(p, sp, s);
   return (int)cudaGetLastError();
 }
 
-int launch_kv4_read(const Kv4ReadParams& p, void* stream) {
-  const unsigned grid = (unsigned)blocks_for(p.c, 2 * p.c.kv_heads);
+int launch_kv4_read(Kv4ReadParams p, void* stream) {
+  const Spread sp = spread(p.c, 2 * p.c.kv_heads);
+  p.warps_per_token = sp.warps_per_token;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.c.dim == 128) {
-    if (p.bf16) read_kernel<128, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else read_kernel<128, float><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (p.bf16) read_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else read_kernel<64, float><<<grid, kThreads, 0, s>>>(p);
-  }
+  if (p.c.dim == 128) p.bf16 ? read_any<128, __nv_bfloat16>(p, sp, s) : read_any<128, float>(p, sp, s);
+  else p.bf16 ? read_any<64, __nv_bfloat16>(p, sp, s) : read_any<64, float>(p, sp, s);
   return (int)cudaGetLastError();
 }
 
@@ -273,7 +351,7 @@ extern "C" tern_status tern_kv4_append(const tern_kv4_cache* cache, const tern_k
       (heads > 0 && (!aligned16(d_q) || !aligned16(d_q_out))))
     return TERN_EALIGN;
   p.c.heads = heads;
-  if (blocks_for(p.c, heads + 2 * p.c.kv_heads) > 0x7FFFFFFFll) return TERN_EINVAL;
+  if (spread(p.c, heads + 2 * p.c.kv_heads).blocks > 0x7FFFFFFFll) return TERN_EINVAL;
   p.q = d_q;
   p.k = d_k;
   p.v = d_v;
@@ -298,7 +376,7 @@ extern "C" tern_status tern_kv4_read(const tern_kv4_cache* cache, const tern_kv4
   if ((d_k && (ldk < kvw || (ldk & 7) != 0)) || (d_v && (ldv < kvw || (ldv & 7) != 0))) return TERN_EINVAL;
   if ((d_k && !aligned16(d_k)) || (d_v && !aligned16(d_v))) return TERN_EALIGN;
   if (p.c.seqs == 0 || p.c.tokens == 0 || p.c.max_new == 0 || (!d_k && !d_v)) return TERN_OK;
-  if (blocks_for(p.c, 2 * p.c.kv_heads) > 0x7FFFFFFFll) return TERN_EINVAL;
+  if (spread(p.c, 2 * p.c.kv_heads).blocks > 0x7FFFFFFFll) return TERN_EINVAL;
   p.k = d_k;
   p.v = d_v;
   p.ldk = ldk;
