@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_u32(smem), pad = (1024u - (base & 1023u)) & 1023u;
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + pad);
   const uint32_t ring = base + pad + kCtlBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   volatile uint32_t* misc = ctl.misc;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = ctl.misc[tc::kMiscTmem];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.misc[tc::kMiscTmem], 0);
   // a tile's CTAs are a cluster of pl.split consecutive ones
   const int rank = pl.split > 1 ? (int)(blockIdx.x % pl.split) : 0;
   const int first = (int)blockIdx.x / pl.split, stride = (int)gridDim.x / pl.split;
@@ -147,35 +147,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = tc::idesc_i8_s32(pl.tn);
-      int stage = 0, seg = 0;
-      uint32_t ph = 0;
-      for (int tile = first; tile < pl.tiles && !misc[tc::kMiscAbort]; tile += stride, ++seg) {
-        const int buf = seg & 1;
-        if (seg >= 2 && !tc::tc_wait(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u, misc)) break;
+    // the whole warp in step, one lane of it issuing
+    const uint32_t idesc = tc::idesc_i8_s32(pl.tn), lead = lane == 0 ? 1u : 0u;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::tc_wait(bar, parity, misc)); };
+    int stage = 0, seg = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int tile = first; tile < pl.tiles && ok; tile += stride, ++seg) {
+      const int buf = seg & 1;
+      if (seg >= 2) ok = wait(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u);
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + (uint32_t)(buf * pl.tn);
+      for (int k = k0; k < k1 && ok; ++k) {
+        ok = wait(&ctl.full[stage], ph);
         tc::fence_after_sync();
-        const uint32_t acc = tmem + (uint32_t)(buf * pl.tn);
-        for (int k = k0; k < k1; ++k) {
-          if (!tc::tc_wait(&ctl.full[stage], ph, misc)) break;
-          tc::fence_after_sync();
-          const uint32_t st = ring + (uint32_t)(stage * pl.stage_bytes);
-          const uint64_t ad = tc::smem_desc_sw128(st), bd = tc::smem_desc_sw128(st + kBytesA);
+        const uint32_t st = ring + (uint32_t)(stage * pl.stage_bytes);
+        const uint64_t ad = tc::smem_desc_sw128(st), bd = tc::smem_desc_sw128(st + kBytesA);
 #pragma unroll
-          for (int i = 0; i < kStepK / 32; ++i)  // 32 bytes of K: two 16-byte units of the start address
-            tc::mma_i8(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u);
-          tc::commit(&ctl.empty[stage]);
-          if (++stage == pl.stages) {
-            stage = 0;
-            ph ^= 1u;
-          }
+        for (int i = 0; i < kStepK / 32; ++i)  // 32 bytes of K: two 16-byte units of the start address
+          tc::mma_i8_lead(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u, ok ? lead : 0u);
+        tc::commit_lead(&ctl.empty[stage], lead);
+        if (++stage == pl.stages) {
+          stage = 0;
+          ph ^= 1u;
         }
-        tc::commit(&ctl.acc_full[buf]);
       }
-      // every MMA issued has completed before tensor memory is released
-      tc::commit(&ctl.fin);
-      mbar_wait_bounded(&ctl.fin, 0u);
+      tc::commit_lead(&ctl.acc_full[buf], lead);
     }
+    // every MMA issued has completed before tensor memory is released
+    tc::commit_lead(&ctl.fin, lead);
+    mbar_wait_bounded(&ctl.fin, 0u);
   } else if (warp >= 4) {
     const int q4 = warp & 3, et = threadIdx.x - 128;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;

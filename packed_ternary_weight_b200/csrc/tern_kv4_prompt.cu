@@ -50,7 +50,7 @@ namespace {
 using kv4::ex2;
 using kv4::exp2i;
 
-constexpr int kWarps = 13;
+constexpr int kWarps = 16;  // of them 13-15 idle: register shares move between groups of four warps
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 128;             // positions
 constexpr int kRows = 256;              // query rows of a unit
@@ -66,6 +66,7 @@ struct Ctl {
   alignas(16) uint32_t absent[4][4];  // positions of block (its number mod 4) that a bad page leaves out, a bit each
   alignas(16) uint32_t poison[4][4];  // positions whose values are not finite
   kv4::ShareScratch<kWarps> share;
+  kv4::Share mine;  // this CTA's share
   int last;
 };
 constexpr int kCtlBytes = 1024;
@@ -95,21 +96,22 @@ __device__ __forceinline__ long long seq_blocks(const Kv4PromptParams& p, const 
 
 // Walks a CTA's share, segment by segment; every role has its own.
 struct Walk {
-  long long at, stop, in_tile;
-  int s, tile;
+  long long at, stop;
+  int s, tile, h, b;  // where the next segment begins
   kv4::Seq q;
   __device__ __forceinline__ Walk(const Kv4PromptParams& p, const kv4::Share& sh)
-      : at(sh.at), stop(sh.stop), in_tile(sh.in_seq), s(sh.s), tile(0), q(kv4::load_seq(p.c, sh.s)) {
-    skip(p);
-  }
-  // past the tiles that end before the place
-  __device__ __forceinline__ void skip(const Kv4PromptParams& p) {
+      : at(sh.at), stop(sh.stop), s(sh.s), tile(0), h(0), b(0), q(kv4::load_seq(p.c, sh.s)) {
+    long long left = sh.in_seq;  // blocks of the sequence before the place
     const int tiles = seq_tiles(p, q);
-    while (tile < tiles) {
-      const long long span = (long long)unit_blocks(p, q, tile) * p.c.kv_heads;
-      if (in_tile < span) return;
-      in_tile -= span;
-      ++tile;
+    for (; tile < tiles; ++tile) {
+      const int blocks = unit_blocks(p, q, tile);
+      const long long span = (long long)blocks * p.c.kv_heads;
+      if (left < span) {
+        h = (int)(left / blocks);
+        b = (int)(left - (long long)h * blocks);
+        break;
+      }
+      left -= span;
     }
   }
   __device__ __forceinline__ bool next(const Kv4PromptParams& p, Segment* g) {
@@ -117,24 +119,26 @@ struct Walk {
     while (!q.ok || q.n * p.group < p.min_rows || tile >= seq_tiles(p, q)) {
       if (++s >= p.c.seqs) return false;
       q = kv4::load_seq(p.c, s);
-      tile = 0;
-      in_tile = 0;
+      tile = h = b = 0;
     }
     const int blocks = unit_blocks(p, q, tile);
     g->q = q;
     g->s = s;
-    g->h = (int)(in_tile / blocks);
-    g->b0 = (int)(in_tile - (long long)g->h * blocks);
-    g->b1 = (int)min((long long)blocks, g->b0 + (stop - at));
+    g->h = h;
+    g->b0 = b;
+    g->b1 = (int)min((long long)blocks, b + (stop - at));
     g->blocks = blocks;
     g->row_first = tile * kRows;
     g->rows = min(kRows, q.n * p.group - g->row_first);
-    g->unit_first = at - g->b0;
-    at += g->b1 - g->b0;
-    in_tile += g->b1 - g->b0;
-    if (in_tile >= (long long)blocks * p.c.kv_heads) {
-      in_tile = 0;
-      ++tile;
+    g->unit_first = at - b;
+    at += g->b1 - b;
+    b = g->b1;
+    if (b >= blocks) {
+      b = 0;
+      if (++h >= p.c.kv_heads) {
+        h = 0;
+        ++tile;
+      }
     }
     return true;
   }
@@ -144,6 +148,24 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;"
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
@@ -182,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + pad);
   const uint32_t qs = base + pad + kCtlBytes, ks = qs + 2 * kOperand, vs = ks + 2 * kOperand;
   const Kv4Params& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   volatile uint32_t* misc = ctl.misc;
 
   kv4::Share sh;
@@ -207,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
     mbar_init(&ctl.fin, 1);
     ctl.misc[tc::kMiscAbort] = 0;
+    ctl.mine = sh;
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -216,12 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = ctl.misc[tc::kMiscTmem];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.misc[tc::kMiscTmem], 0);
   Walk walk(p, sh);
   Segment g;
+  // the waits of whole warps: suspended by the hardware, bounded, given up at once after another's expiry
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!misc[tc::kMiscAbort] && !mbar_wait_bounded(bar, parity)) misc[tc::kMiscAbort] = 1u;
+  };
 
+  // The 512 threads start with 128 registers each, the whole file. Shares per
+  // group of four warps: 152 + 152 (softmax) + 112 + 96 = 4 x 128.
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)(128 * x), o_col = tmem + lanes + 256u + (uint32_t)(128 * x);
@@ -252,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
         }
         const int ex = max(-100, (__float_as_int(big) >> 23) - 127);
         const float f = p.scale_log2 < 0.f ? -exp2i(14 - ex) : exp2i(14 - ex);
-        rowf = exp2i(min(127, ex - 14)) * fabsf(p.scale_log2);
+        rowf = fmaxf(exp2i(min(127, ex - 14)) * fabsf(p.scale_log2), 1e-30f);  // above zero: masked scores stay -inf
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           const uint4 u = load(i);
@@ -268,33 +298,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       }
       for (int b = g.b0; b < g.b1; ++b, ++block) {
         if (!here) continue;
-        tc::tc_wait_many(&ctl.s_full[x], s_ph, misc);
+        wait(&ctl.s_full[x], s_ph);
         s_ph ^= 1u;
         tc::fence_after_sync();
         const int seen = limit - b * kBlock;  // of this block's positions
-        const uint4 ab = *reinterpret_cast<const uint4*>(ctl.absent[block & 3]),
-                    po = *reinterpret_cast<const uint4*>(ctl.poison[block & 3]);
-        const bool odd = (ab.x | ab.y | ab.z | ab.w | po.x | po.y | po.z | po.w) != 0u;
+        const uint32_t* ab = ctl.absent[block & 3];
+        const uint32_t* po = ctl.poison[block & 3];
+        const bool odd = (ab[0] | ab[1] | ab[2] | ab[3] | po[0] | po[1] | po[2] | po[3]) != 0u;
         const bool plain = __all_sync(0xffffffffu, seen >= kBlock && !odd);
-        auto hidden = [&](int j) {  // of a masked block: is position j hidden from the row?
-          const uint32_t w = j < 32 ? ab.x : (j < 64 ? ab.y : (j < 96 ? ab.z : ab.w));
-          return j >= seen || ((w >> (j & 31)) & 1u);
+        auto visible = [&](int q) {  // a bit for each of the positions 32 q .. 32 q + 31
+          const int n = seen - 32 * q;
+          return (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u)) & ~ab[q];
         };
-        float mx = -INFINITY;
+        // the rows' maxima first, 32 positions at a time with the next ones on their way; a row whose maximum has
+        // passed its reference by too much (the first block, hardly ever later) is rescaled
+        uint32_t v[2][32];
+        auto mask = [&](uint32_t (&u)[32], int q) {
+          if (!plain) {
+            const uint32_t vis = visible(q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tc::ld_x32_sync(s_col + 32 * q, v);
-          if (plain) {
+            for (int i = 0; i < 32; ++i) u[i] = (vis >> i) & 1u ? u[i] : 0xFF800000u;  // minus infinity
+          }
+        };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tc::ld_x32(s_col, v[0]);
+#pragma unroll 1  // short loops: four roles share the instruction caches
+        for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-          } else {
+          for (int h = 0; h < 2; ++h) {
+            uint32_t(&u)[32] = v[h];
+            tc::ld_wait_x32(u);
+            tc::ld_x32(s_col + 32 * ((q + h + 1) & 3), v[h ^ 1]);
+            mask(u, q + h);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!hidden(32 * q + i)) mx = fmaxf(mx, __uint_as_float(v[i]));
+            for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(u[i + k])), __uint_as_float(u[i + 4 + k]));
+            }
           }
         }
-        const float top = mx == -INFINITY ? -INFINITY : mx * rowf;
+        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = most == -INFINITY ? -INFINITY : most * rowf;
         const bool grow = top > ref + kGrowth || (ref == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
           const float next = fmaxf(ref, top);
@@ -302,38 +347,46 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
           ref = next;
           l *= f;
           if (b > g.b0) {  // the last block's product is complete: the scores came after it
+            tc::ld_wait_x32(v[0]);
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t v[16];
-              tc::ld_x16_sync(o_col + 16 * q, v);
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t h[16];
+              tc::ld_x16_sync(o_col + 16 * i, h);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tc::st_x16(o_col + 16 * q, v);
+              for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * f);
+              tc::st_x16(o_col + 16 * i, h);
             }
           }
         }
+        // then the probabilities, into the first half of the scores' columns
         const float bias = kShift - (ref == -INFINITY ? 0.f : ref);
+        const float2 rowf2 = make_float2(rowf, rowf), bias2 = make_float2(bias, bias);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32], w[16];
-          tc::ld_x32_sync(s_col + 32 * q, v);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t(&u)[32] = v[h];
+            tc::ld_wait_x32(u);
+            // after the last columns the first ones again, into registers that nothing reads
+            tc::ld_x32(s_col + 32 * ((q + h + 1) & 3), v[h ^ 1]);
+            mask(u, q + h);
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float e0 = ex2(fmaf(__uint_as_float(v[i]), rowf, bias)), e1 = ex2(fmaf(__uint_as_float(v[i + 1]), rowf, bias));
-            if (!plain) {
-              if (hidden(32 * q + i)) e0 = 0.f;
-              if (hidden(32 * q + i + 1)) e1 = 0.f;
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = fma2(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), rowf2, bias2);
+              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], e);
+              w[i / 2] = pack_half2(e.x, e.y);
             }
-            l += e0 + e1;
-            w[i / 2] = pack_half2(e0, e1);
+            tc::st_x16(s_col + 16 * (q + h), w);
           }
-          tc::st_x16(s_col + 16 * q, w);
         }
+        tc::ld_wait_x32(v[0]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (odd) {  // a visible value that is not finite makes the row so
-          for (int j = 0; j < kBlock; ++j) {
-            const uint32_t w = j < 32 ? po.x : (j < 64 ? po.y : (j < 96 ? po.z : po.w));
-            if (((w >> (j & 31)) & 1u) && !hidden(j)) l = NAN;
-          }
+          for (int q = 0; q < 4; ++q)
+            if (po[q] & visible(q)) l = NAN;
         }
         tc::st_wait();
         tc::fence_before_sync();
@@ -341,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
         if (lane == 0) tc::mbar_arrive(&ctl.p_full[x]);
       }
       // ---- the segment's end: the output, or a part of it
-      const int first_cta = sh.cta_of(g.unit_first), last_cta = sh.cta_of(g.unit_first + g.blocks - 1);
+      const int first_cta = ctl.mine.cta_of(g.unit_first), last_cta = ctl.mine.cta_of(g.unit_first + g.blocks - 1);
       const bool whole = first_cta == last_cta;
       constexpr size_t kSlot = (size_t)kRows * (D + 2);  // floats: [D / 4][256][4], then (reference, sum) [256]
       float* part = p.part + (size_t)(2 * blockIdx.x + (g.b0 == 0 ? 1 : 0)) * kSlot;
@@ -355,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
         *reinterpret_cast<uint4*>(p.out + at + 8 * i) = make_uint4(two(0, 2), two(4, 6), two(1, 3), two(5, 7));
       };
       if (here) {
-        tc::tc_wait_many(&ctl.o_full[x], o_ph, misc);
+        wait(&ctl.o_full[x], o_ph);
         tc::fence_after_sync();
 #pragma unroll 1
         for (int q = 0; q < D / 16; ++q) {
@@ -421,109 +474,161 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
   } else if (warp < 12) {
     // ------------------------------------------------- codes -> operands
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    // Three steps in flight: the page of block i + 2, the codes of block i + 1, block i into shared memory.
     const int tid = threadIdx.x - 256;  // position within a block
-    int block = 0;
-    while (walk.next(p, &g)) {
-      for (int b = g.b0; b < g.b1; ++b, ++block) {
-        const int pos = b * kBlock + tid, stage = block & 1;
-        const bool inside = pos < g.q.len;
-        int page = -1;
-        if (inside) {
-          page = kv4::page_of(c, g.s, pos);
-          if (page < 0) kv4::report_bad();
-        }
-        uint4 kw[D / 32], vw[D / 32];
-        uint2 pair = make_uint2(0, 0);
+    struct {
+      bool valid, inside;
+      int page, slot, h;
+    } ahead;
+    int b = 0, b1 = 0;
+    auto look_up = [&] {  // the next block of the share
+      if (b == b1) {
+        ahead.valid = walk.next(p, &g);
+        if (!ahead.valid) return;
+        b = g.b0;
+        b1 = g.b1;
+      }
+      const int pos = b * kBlock + tid;
+      ahead.valid = true;
+      ahead.inside = pos < g.q.len;
+      ahead.page = ahead.inside ? __ldg(c.table + (size_t)g.s * c.max_pages + (pos >> c.log_page)) : -1;
+      ahead.slot = pos & (c.page - 1);
+      ahead.h = g.h;
+      ++b;
+    };
+    uint4 kn[D / 32], vn[D / 32];
+    uint2 pn = make_uint2(0, 0);
+    bool valid, absent = false;
+    auto load = [&] {
+      valid = ahead.valid;
+      if (!valid) return;
+      const bool there = (unsigned)ahead.page < (unsigned)c.num_pages;
+      absent = ahead.inside && !there;
+      if (absent) kv4::report_bad();
+      pn = make_uint2(0, 0);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-          const uint8_t* blk = c.pages + kv4::block_offset(c, page, g.h);
-          const int slot = pos & (c.page - 1);
-          const uint4* kr = reinterpret_cast<const uint4*>(blk + (size_t)slot * (D / 2));
-          const uint4* vr = reinterpret_cast<const uint4*>(blk + (size_t)(c.page + slot) * (D / 2));
+      for (int i = 0; i < D / 32; ++i) kn[i] = vn[i] = make_uint4(0, 0, 0, 0);
+      if (there) {
+        const uint8_t* blk = c.pages + kv4::block_offset(c, ahead.page, ahead.h);
+        const uint4* kr = reinterpret_cast<const uint4*>(blk + (size_t)ahead.slot * (D / 2));
+        const uint4* vr = reinterpret_cast<const uint4*>(blk + (size_t)(c.page + ahead.slot) * (D / 2));
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) kw[i] = __ldg(kr + i), vw[i] = __ldg(vr + i);
-          pair = __ldg(reinterpret_cast<const uint2*>(blk + (size_t)c.page * D + (size_t)slot * 8));
+        for (int i = 0; i < D / 32; ++i) kn[i] = __ldg(kr + i), vn[i] = __ldg(vr + i);
+        pn = __ldg(reinterpret_cast<const uint2*>(blk + (size_t)c.page * D + (size_t)ahead.slot * 8));
+      }
+    };
+    look_up();
+    load();
+    if (valid) look_up();
+    for (int block = 0; valid; ++block) {
+      const int stage = block & 1;
+      uint4 kw[D / 32], vw[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) kw[i] = kn[i], vw[i] = vn[i];
+      const uint2 pair = pn;
+      const float2 vp = __half22float2(as_half2(pair.y));
+      const bool bad_value = !(fabsf(vp.y) + 15.f * fabsf(vp.x) < 65520.f);  // as fp16, or not a number
+      const uint32_t ab = __ballot_sync(0xffffffffu, absent), po = __ballot_sync(0xffffffffu, bad_value);
+      load();
+      if (valid) look_up();
+#pragma unroll 1  // keys, then values: one copy of the code
+      for (int which = 0; which < 2; ++which) {
+        if (block >= 2)
+          wait(which == 0 ? &ctl.k_empty[stage] : &ctl.v_empty[stage], (uint32_t)(block / 2 - 1) & 1u);
+        if (which == 0) {
+          if (lane == 0) {
+            ctl.absent[block & 3][tid >> 5] = ab;
+            ctl.poison[block & 3][tid >> 5] = po;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) kw[i] = vw[i];
         }
-        const float2 vp = __half22float2(as_half2(pair.y));
-        const bool bad_value = !(fabsf(vp.y) + 15.f * fabsf(vp.x) < 65520.f);  // as fp16, or not a number
-        const uint32_t ab = __ballot_sync(0xffffffffu, inside && page < 0);
-        const uint32_t po = __ballot_sync(0xffffffffu, bad_value);
-        if (block >= 2) tc::tc_wait_many(&ctl.k_empty[stage], (uint32_t)(block / 2 - 1) & 1u, misc);
-        if (lane == 0) {
-          ctl.absent[block & 3][tid >> 5] = ab;
-          ctl.poison[block & 3][tid >> 5] = po;
-        }
-        expand<D>(ks + (uint32_t)(stage * kOperand), tid, kw, pair.x);
+        expand<D>((which == 0 ? ks : vs) + (uint32_t)(stage * kOperand), tid, kw,
+                  which == 0 ? pair.x : (bad_value ? 0u : pair.y));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.k_full[stage]);
-        if (block >= 2) tc::tc_wait_many(&ctl.v_empty[stage], (uint32_t)(block / 2 - 1) & 1u, misc);
-        expand<D>(vs + (uint32_t)(stage * kOperand), tid, vw, bad_value ? 0u : pair.y);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ctl.v_full[stage]);
+        if (lane == 0) tc::mbar_arrive(which == 0 ? &ctl.k_full[stage] : &ctl.v_full[stage]);
       }
     }
   } else {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == 12) {
+      // the whole warp in step, one lane of it issuing
       constexpr uint32_t id_s = tc::idesc_f16_f32(kBlock, false), id_o = tc::idesc_f16_f32(D, true);
-      int block = 0;
-      uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0}, o_uses[2] = {0, 0};
-      auto scores = [&](int x, int stage) {
-        const uint32_t a = qs + (uint32_t)(x * kOperand), b = ks + (uint32_t)(stage * kOperand);
+      const uint32_t lead = lane == 0 ? 1u : 0u;
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, tc::tc_wait(bar, parity, misc)) && ok;
+      };
+      uint32_t block = 0, p_ph[2] = {0, 0}, q_ph[2] = {0, 0}, o_uses[2] = {0, 0};
+      // descriptors: an address offset adds to the field in units of 16 bytes
+      const uint64_t dq = tc::smem_desc_sw128(qs), dk = tc::smem_desc_sw128(ks), dv = tc::smem_desc_sw128_mn(vs, kSub);
+      auto scores = [&](int x, uint32_t stage) {
+        const uint64_t a = dq + (uint32_t)(x * (kOperand >> 4)), k = dk + stage * (uint32_t)(kOperand >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t o = (uint32_t)((i / 4) * kSub + (i % 4) * 32);
-          tc::mma_f16_ss(tmem + (uint32_t)(128 * x), tc::smem_desc_sw128(a + o), tc::smem_desc_sw128(b + o), id_s,
-                         i > 0 ? 1u : 0u);
+          const uint32_t o = (uint32_t)(((i / 4) * kSub + (i % 4) * 32) >> 4);
+          tc::mma_f16_ss(tmem + (uint32_t)(128 * x), a + o, k + o, id_s, i > 0 ? 1u : 0u, lead);
         }
-        tc::commit(&ctl.s_full[x]);
+        tc::commit_lead(&ctl.s_full[x], lead);
       };
-      while (walk.next(p, &g) && !misc[tc::kMiscAbort]) {
-        const int nsub = g.rows > kHalf ? 2 : 1;
-        tc::tc_wait(&ctl.k_full[block & 1], (uint32_t)(block / 2) & 1u, misc);
-        for (int x = 0; x < nsub; ++x) {
-          tc::tc_wait(&ctl.q_full[x], q_ph[x], misc);
-          q_ph[x] ^= 1u;
-          tc::fence_after_sync();
-          scores(x, block & 1);
+      auto values = [&](int x, uint32_t stage, uint32_t more) {
+        const uint64_t v = dv + stage * (uint32_t)(kOperand >> 4);
+#pragma unroll
+        for (int i = 0; i < kBlock / 16; ++i)
+          tc::mma_f16_ts(tmem + 256u + (uint32_t)(128 * x), tmem + (uint32_t)(128 * x + 8 * i), v + (uint32_t)(i * 128),
+                         id_o, i > 0 ? 1u : more, lead);
+      };
+      while (walk.next(p, &g)) {
+        const int nsub = __shfl_sync(0xffffffffu, g.rows > kHalf ? 2 : 1, 0);
+        const int blocks = __shfl_sync(0xffffffffu, g.b1 - g.b0, 0);
+        wait_all(&ctl.k_full[block & 1], (block / 2) & 1u);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x < nsub) {
+            wait_all(&ctl.q_full[x], q_ph[x]);
+            q_ph[x] ^= 1u;
+            tc::fence_after_sync();
+            if (!ok) break;
+            scores(x, block & 1);
+          }
         }
-        tc::commit(&ctl.k_empty[block & 1]);
-        for (int b = g.b0; b < g.b1; ++b, ++block) {
-          if (misc[tc::kMiscAbort]) break;
-          const bool more = b + 1 < g.b1;
-          tc::tc_wait(&ctl.v_full[block & 1], (uint32_t)(block / 2) & 1u, misc);
-          for (int x = 0; x < nsub; ++x) {
-            tc::tc_wait(&ctl.p_full[x], p_ph[x], misc);
+        tc::commit_lead(&ctl.k_empty[block & 1], lead);
+        for (int b = 0; b < blocks && ok; ++b, ++block) {
+          const bool more = b + 1 < blocks;
+          wait_all(&ctl.v_full[block & 1], (block / 2) & 1u);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x >= nsub) break;
+            wait_all(&ctl.p_full[x], p_ph[x]);
             p_ph[x] ^= 1u;
             // the accumulator's last user has read it
-            if (b == g.b0 && o_uses[x] > 0) tc::tc_wait(&ctl.o_free[x], (o_uses[x] - 1) & 1u, misc);
+            if (b == 0 && o_uses[x] > 0) wait_all(&ctl.o_free[x], (o_uses[x] - 1) & 1u);
             tc::fence_after_sync();
-            const uint32_t v = vs + (uint32_t)((block & 1) * kOperand);
-#pragma unroll
-            for (int i = 0; i < kBlock / 16; ++i)
-              tc::mma_f16_ts(tmem + 256u + (uint32_t)(128 * x), tmem + (uint32_t)(128 * x + 8 * i),
-                             tc::smem_desc_sw128_mn(v + (uint32_t)(i * 16 * 128), kSub), id_o,
-                             b > g.b0 || i > 0 ? 1u : 0u);
+            if (!ok) break;
+            values(x, block & 1, b > 0 ? 1u : 0u);
             if (more) {
               if (x == 0) {
-                tc::tc_wait(&ctl.k_full[(block + 1) & 1], (uint32_t)((block + 1) / 2) & 1u, misc);
+                wait_all(&ctl.k_full[(block + 1) & 1], ((block + 1) / 2) & 1u);
                 tc::fence_after_sync();
+                if (!ok) break;
               }
               scores(x, (block + 1) & 1);
             } else {
-              tc::commit(&ctl.o_full[x]);
+              tc::commit_lead(&ctl.o_full[x], lead);
               ++o_uses[x];
             }
           }
-          tc::commit(&ctl.v_empty[block & 1]);
-          if (more) tc::commit(&ctl.k_empty[(block + 1) & 1]);
+          tc::commit_lead(&ctl.v_empty[block & 1], lead);
+          if (more) tc::commit_lead(&ctl.k_empty[(block + 1) & 1], lead);
         }
+        if (!ok) break;
       }
       // every MMA issued has completed before tensor memory is released
-      tc::commit(&ctl.fin);
+      tc::commit_lead(&ctl.fin, lead);
       mbar_wait_bounded(&ctl.fin, 0u);
     }
   }
