@@ -194,6 +194,28 @@ __device__ __forceinline__ void expand(uint32_t dst, int row, const uint4 (&w)[D
   }
 }
 
+// Multiplies what a row has so far by f: `parts` times 32 probabilities at s_col
+// and the accumulator at o_col (0: there is none yet).
+template <int D>
+__device__ __noinline__ void rescale(uint32_t s_col, int parts, float f, uint32_t o_col) {
+  const __half2 f2 = __float2half2_rn(f);
+  uint32_t h[16];
+#pragma unroll 1
+  for (int i = 0; i < parts; ++i) {
+    tc::ld_x16_sync(s_col + 16 * i, h);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k] = as_u32(__hmul2(as_half2(h[k]), f2));
+    tc::st_x16(s_col + 16 * i, h);
+  }
+#pragma unroll 1
+  for (int i = 0; o_col != 0u && i < D / 16; ++i) {
+    tc::ld_x16_sync(o_col + 16 * i, h);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * f);
+    tc::st_x16(o_col + 16 * i, h);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptParams p) {
   constexpr int SUBS = D / 64;            // 64-dimension parts of an operand
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   // group of four warps: 152 + 152 (softmax) + 112 + 96 = 4 x 128.
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)(128 * x), o_col = tmem + lanes + 256u + (uint32_t)(128 * x);
@@ -268,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       const bool here = x < nsub;
       if (here) {
         // q, times a power of two, in the swizzled layout
-        auto load = [&](int i) {
-          return live ? reinterpret_cast<const uint4*>(p.q + at)[i] : make_uint4(0, 0, 0, 0);
-        };
+        uint4 u[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          u[i] = live ? reinterpret_cast<const uint4*>(p.q + at)[i] : make_uint4(0, 0, 0, 0);
         float big = 0.f;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          const uint4 u = load(i);
-          const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             big = fmaxf(big, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
@@ -283,10 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
         const int ex = max(-100, (__float_as_int(big) >> 23) - 127);
         const float f = p.scale_log2 < 0.f ? -exp2i(14 - ex) : exp2i(14 - ex);
         rowf = fmaxf(exp2i(min(127, ex - 14)) * fabsf(p.scale_log2), 1e-30f);  // above zero: masked scores stay -inf
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          const uint4 u = load(i);
-          const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
           auto lo = [&](int k) { return __uint_as_float(e[k] << 16) * f; };
           auto hi = [&](int k) { return __uint_as_float(e[k] & 0xFFFF0000u) * f; };
           tc::sts128(qs + (uint32_t)(x * kOperand + (i / 8) * kSub) + piece(row, i % 8), pack_half2(lo(0), lo(2)),
@@ -310,59 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
           const int n = seen - 32 * q;
           return (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u)) & ~ab[q];
         };
-        // the rows' maxima first, 32 positions at a time with the next ones on their way; a row whose maximum has
-        // passed its reference by too much (the first block, hardly ever later) is rescaled
-        uint32_t v[2][32];
-        auto mask = [&](uint32_t (&u)[32], int q) {
-          if (!plain) {
-            const uint32_t vis = visible(q);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = (vis >> i) & 1u ? u[i] : 0xFF800000u;  // minus infinity
-          }
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tc::ld_x32(s_col, v[0]);
-#pragma unroll 1  // short loops: four roles share the instruction caches
-        for (int q = 0; q < 4; q += 2) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t(&u)[32] = v[h];
-            tc::ld_wait_x32(u);
-            tc::ld_x32(s_col + 32 * ((q + h + 1) & 3), v[h ^ 1]);
-            mask(u, q + h);
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(u[i + k])), __uint_as_float(u[i + 4 + k]));
-            }
-          }
-        }
-        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float top = most == -INFINITY ? -INFINITY : most * rowf;
-        const bool grow = top > ref + kGrowth || (ref == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float next = fmaxf(ref, top);
-          const float f = ref == -INFINITY ? 0.f : ex2(ref - next);
-          ref = next;
-          l *= f;
-          if (b > g.b0) {  // the last block's product is complete: the scores came after it
-            tc::ld_wait_x32(v[0]);
-#pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t h[16];
-              tc::ld_x16_sync(o_col + 16 * i, h);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * f);
-              tc::st_x16(o_col + 16 * i, h);
-            }
-          }
-        }
-        // then the probabilities, into the first half of the scores' columns
-        const float bias = kShift - (ref == -INFINITY ? 0.f : ref);
-        const float2 rowf2 = make_float2(rowf, rowf), bias2 = make_float2(bias, bias);
+        // 32 positions at a time, each score read once, the next ones on their way; a row whose maximum has passed
+        // its reference by too much (the first block, hardly ever later) is rescaled
+        const float2 rowf2 = make_float2(rowf, rowf);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
+        uint32_t v[2][32];
+        tc::ld_x32(s_col, v[0]);
+#pragma unroll 1  // a short loop: four roles share the instruction caches
         for (int q = 0; q < 4; q += 2) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -370,7 +345,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
             tc::ld_wait_x32(u);
             // after the last columns the first ones again, into registers that nothing reads
             tc::ld_x32(s_col + 32 * ((q + h + 1) & 3), v[h ^ 1]);
-            mask(u, q + h);
+            if (!plain) {
+              const uint32_t vis = visible(q + h);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] = (vis >> i) & 1u ? u[i] : 0xFF800000u;  // minus infinity
+            }
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(u[k]), __uint_as_float(u[4 + k]));
+#pragma unroll
+            for (int i = 8; i < 32; i += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(u[i + k])), __uint_as_float(u[i + 4 + k]));
+            }
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const float top = most == -INFINITY ? -INFINITY : most * rowf;
+            const bool grow = top > ref + kGrowth || (ref == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float next = fmaxf(ref, top);
+              const float f = ref == -INFINITY ? 0.f : ex2(ref - next);
+              ref = next;
+              l *= f;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) sum[k] = make_float2(sum[k].x * f, sum[k].y * f);
+              rescale<D>(s_col, q + h, f, b > g.b0 ? o_col : 0u);
+            }
+            const float bias = kShift - (ref == -INFINITY ? 0.f : ref);
+            const float2 bias2 = make_float2(bias, bias);
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -455,18 +457,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
             sum = fmaf(e.x == -INFINITY ? 0.f : ex2(e.x - top), e.y, sum);
           }
 #pragma unroll 1
-          for (int q = 0; q < D / 8; ++q) {
-            float o[8] = {};
-#pragma unroll 4
+          for (int q = 0; q < D / 32; ++q) {  // 32 columns, eight loads in flight
+            float o[4][8] = {};
+#pragma unroll 1
             for (int i = 0; i < ns; ++i) {
+              const float4* src = reinterpret_cast<const float4*>(slot(i)) + (8 * q) * kRows + prow;
               const float e = __ldcg(reinterpret_cast<const float2*>(slot(i) + (size_t)kRows * D) + prow).x;
+              float4 a[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) a[k] = __ldcg(src + k * kRows);
               const float f = e == -INFINITY ? 0.f : ex2(e - top);
-              const float4* src = reinterpret_cast<const float4*>(slot(i));
-              const float4 a = __ldcg(src + (2 * q) * kRows + prow), d = __ldcg(src + (2 * q + 1) * kRows + prow);
-              o[0] = fmaf(f, a.x, o[0]), o[1] = fmaf(f, a.y, o[1]), o[2] = fmaf(f, a.z, o[2]), o[3] = fmaf(f, a.w, o[3]);
-              o[4] = fmaf(f, d.x, o[4]), o[5] = fmaf(f, d.y, o[5]), o[6] = fmaf(f, d.z, o[6]), o[7] = fmaf(f, d.w, o[7]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                float* d = o[k / 2] + 4 * (k & 1);
+                d[0] = fmaf(f, a[k].x, d[0]), d[1] = fmaf(f, a[k].y, d[1]);
+                d[2] = fmaf(f, a[k].z, d[2]), d[3] = fmaf(f, a[k].w, d[3]);
+              }
             }
-            write(q, o, sum);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) write(4 * q + k, o[k], sum);
           }
         }
         sync_softmax();
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
   } else {
     // ------------------------------------------------------------------ MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 12) {
       // the whole warp in step, one lane of it issuing
       constexpr uint32_t id_s = tc::idesc_f16_f32(kBlock, false), id_o = tc::idesc_f16_f32(D, true);
