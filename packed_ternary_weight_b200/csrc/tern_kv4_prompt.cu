@@ -14,17 +14,19 @@
 //
 // Work of a CTA: up to two tiles of 128 query rows (the group of heads that reads
 // one kv head, times consecutive tokens) over a range of blocks of 128 positions.
-//   warps 0-3, 4-7   softmax of the first and second tile, a thread per row:
-//                    scores from tensor memory, probabilities back into the columns
-//                    that the scores held;
-//   warps 8-11       codes -> fp16 in shared memory, a thread per position (128-byte
+//   warps 0-7, 8-15  softmax of the first and second tile, two threads per row, one
+//                    for each half of a block's positions: scores from tensor memory,
+//                    probabilities back into columns that the same half's scores held.
+//                    With one thread per row the softmax of a block took 3000 cycles
+//                    (two warps per scheduler cannot hide its latencies);
+//   warps 16-19      codes -> fp16 in shared memory, a thread per position (128-byte
 //                    swizzle; dimensions in the order 0 4 1 5 2 6 3 7 of every eight, as
 //                    the masks leave them: q is stored in the same order and the
 //                    output's columns are put back when they are written);
-//   warp 12          one thread issues S = Q K^T (both operands in shared memory)
-//                    and O += P V (P in tensor memory, V with its dimensions
-//                    contiguous); the two tiles alternate, so that the tensor cores
-//                    work on one while the softmax of the other runs.
+//   warp 20          issues S = Q K^T (both operands in shared memory) and O += P V (P
+//                    in tensor memory, V with its dimensions contiguous); the two
+//                    tiles alternate, so that the tensor cores work on one while the
+//                    softmax of the other runs.
 // Tensor memory: S of the tiles in columns 0 and 128, O in 256 and 384.
 //
 // Split. The blocks that each tile sees are laid end to end and dealt in equal
@@ -50,7 +52,8 @@ namespace {
 using kv4::ex2;
 using kv4::exp2i;
 
-constexpr int kWarps = 16;  // of them 13-15 idle: register shares move between groups of four warps
+constexpr int kWarps = 24;  // of them 21-23 idle: register shares move between groups of four warps
+constexpr int kExpandWarp = 16, kMmaWarp = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 128;             // positions
 constexpr int kRows = 256;              // query rows of a unit
@@ -63,13 +66,15 @@ struct Ctl {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], fin;
   uint32_t misc[4];
+  float top[2][2][128], sum[2][2][128];  // rows' maxima and sums that the two threads of a row exchange
+  float rowf[2][128];                    // what turns a row's scores into exponents
   alignas(16) uint32_t absent[4][4];  // positions of block (its number mod 4) that a bad page leaves out, a bit each
   alignas(16) uint32_t poison[4][4];  // positions whose values are not finite
   kv4::ShareScratch<kWarps> share;
   kv4::Share mine;  // this CTA's share
   int last;
 };
-constexpr int kCtlBytes = 1024;
+constexpr int kCtlBytes = 6 * 1024;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
 // One stretch of blocks [b0, b1) of a unit (sequence, tile of 256 rows, kv head).
@@ -144,7 +149,20 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, 512;" ::: "memory"); }
+// One tile's eight warps (barriers 10 and 11).
+__device__ __forceinline__ void sync_tile(int x) { asm volatile("bar.sync %0, 256;" ::"r"(10 + x) : "memory"); }
+// The two warps that share 32 rows (barriers 1-8): a barrier, and the OR of a predicate over it.
+__device__ __forceinline__ void sync_pair(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool any_pair(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0u;
+}
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -165,6 +183,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
@@ -194,28 +217,6 @@ __device__ __forceinline__ void expand(uint32_t dst, int row, const uint4 (&w)[D
   }
 }
 
-// Multiplies what a row has so far by f: `parts` times 32 probabilities at s_col
-// and the accumulator at o_col (0: there is none yet).
-template <int D>
-__device__ __noinline__ void rescale(uint32_t s_col, int parts, float f, uint32_t o_col) {
-  const __half2 f2 = __float2half2_rn(f);
-  uint32_t h[16];
-#pragma unroll 1
-  for (int i = 0; i < parts; ++i) {
-    tc::ld_x16_sync(s_col + 16 * i, h);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) h[k] = as_u32(__hmul2(as_half2(h[k]), f2));
-    tc::st_x16(s_col + 16 * i, h);
-  }
-#pragma unroll 1
-  for (int i = 0; o_col != 0u && i < D / 16; ++i) {
-    tc::ld_x16_sync(o_col + 16 * i, h);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * f);
-    tc::st_x16(o_col + 16 * i, h);
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptParams p) {
   constexpr int SUBS = D / 64;            // 64-dimension parts of an operand
@@ -239,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.q_full[i], 4);
+      mbar_init(&ctl.q_full[i], 8);
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], 4);
+      mbar_init(&ctl.p_full[i], 8);
       mbar_init(&ctl.o_full[i], 1);
-      mbar_init(&ctl.o_free[i], 4);
+      mbar_init(&ctl.o_free[i], 8);
       mbar_init(&ctl.k_full[i], 4);
       mbar_init(&ctl.k_empty[i], 1);
       mbar_init(&ctl.v_full[i], 4);
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     ctl.mine = sh;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc::tmem_alloc(smem_u32(&ctl.misc[tc::kMiscTmem]), kTmemCols);
     tc::tmem_relinquish();
   }
@@ -269,125 +270,141 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     if (!misc[tc::kMiscAbort] && !mbar_wait_bounded(bar, parity)) misc[tc::kMiscAbort] = 1u;
   };
 
-  // The 512 threads start with 128 registers each, the whole file. Shares per
-  // group of four warps: 152 + 152 (softmax) + 112 + 96 = 4 x 128.
-  if (warp < 8) {
+  // The 768 threads start with 80 registers each, the whole file. Shares per
+  // group of four warps: 4 x 88 (softmax) + 88 + 40 = 6 x 80.
+  if (warp < kExpandWarp) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    const int x = warp >> 2, row = threadIdx.x & 127;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int x = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127, pair = 1 + 4 * x + (warp & 3);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_col = tmem + lanes + (uint32_t)(128 * x), o_col = tmem + lanes + 256u + (uint32_t)(128 * x);
+    const uint32_t s_col = tmem + lanes + (uint32_t)(128 * x + 64 * half),
+                   o_col = tmem + lanes + 256u + (uint32_t)(128 * x + (D / 2) * half);
     uint32_t s_ph = 0, o_ph = 0;
     int block = 0;  // blocks this CTA has seen
     while (walk.next(p, &g)) {
       const int nsub = g.rows > kHalf ? 2 : 1;
       const int rr = g.row_first + kHalf * x + row;  // among the sequence's rows of this kv head
       const bool live = kHalf * x + row < g.rows;
-      const int tok = rr / p.group;
-      const size_t at = ((size_t)(g.q.row0 + tok) * c.heads + (size_t)g.h * p.group + (rr - tok * p.group)) * D;
-      const int limit = live ? g.q.len - g.q.n + tok + 1 : 1 << 30;  // positions the row sees
+      // element offset of one of the sequence's rows of this kv head
+      auto place = [&](int i) {
+        const int t = i / p.group;
+        return ((size_t)(g.q.row0 + t) * c.heads + (size_t)g.h * p.group + (i - t * p.group)) * D;
+      };
+      const int limit = live ? g.q.len - g.q.n + rr / p.group + 1 : 1 << 30;  // positions the row sees
       float ref = -INFINITY, l = 0.f, rowf = 0.f;
       const bool here = x < nsub;
       if (here) {
-        // q, times a power of two, in the swizzled layout
-        uint4 u[D / 8];
+        // q, times a power of two, in the swizzled layout: D / 8 lanes take a row, 16 bytes each
+        constexpr int kPieces = D / 8, kTurns = 128 * kPieces / 256;
+        const int tt = threadIdx.x & 255, pc = tt % kPieces;
+        uint4 u[kTurns];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          u[i] = live ? reinterpret_cast<const uint4*>(p.q + at)[i] : make_uint4(0, 0, 0, 0);
-        float big = 0.f;
+        for (int j = 0; j < kTurns; ++j) {
+          const int r = j * (256 / kPieces) + tt / kPieces;
+          u[j] = kHalf * x + r < g.rows ? *reinterpret_cast<const uint4*>(p.q + place(g.row_first + kHalf * x + r) + 8 * pc)
+                                        : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        for (int j = 0; j < kTurns; ++j) {
+          const int r = j * (256 / kPieces) + tt / kPieces;
+          const uint32_t e[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+          float big = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             big = fmaxf(big, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
-        }
-        const int ex = max(-100, (__float_as_int(big) >> 23) - 127);
-        const float f = p.scale_log2 < 0.f ? -exp2i(14 - ex) : exp2i(14 - ex);
-        rowf = fmaxf(exp2i(min(127, ex - 14)) * fabsf(p.scale_log2), 1e-30f);  // above zero: masked scores stay -inf
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t e[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          for (int k = kPieces / 2; k; k >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+          const int ex = max(-100, (__float_as_int(big) >> 23) - 127);
+          const float f = p.scale_log2 < 0.f ? -exp2i(14 - ex) : exp2i(14 - ex);
+          // above zero: masked scores stay -inf
+          if (pc == 0) ctl.rowf[x][r] = fmaxf(exp2i(min(127, ex - 14)) * fabsf(p.scale_log2), 1e-30f);
           auto lo = [&](int k) { return __uint_as_float(e[k] << 16) * f; };
           auto hi = [&](int k) { return __uint_as_float(e[k] & 0xFFFF0000u) * f; };
-          tc::sts128(qs + (uint32_t)(x * kOperand + (i / 8) * kSub) + piece(row, i % 8), pack_half2(lo(0), lo(2)),
+          tc::sts128(qs + (uint32_t)(x * kOperand + (pc / 8) * kSub) + piece(r, pc % 8), pack_half2(lo(0), lo(2)),
                      pack_half2(hi(0), hi(2)), pack_half2(lo(1), lo(3)), pack_half2(hi(1), hi(3)));
         }
         fence_proxy_async_smem();
-        __syncwarp();
+        sync_tile(x);
         if (lane == 0) tc::mbar_arrive(&ctl.q_full[x]);
+        rowf = ctl.rowf[x][row];
       }
       for (int b = g.b0; b < g.b1; ++b, ++block) {
         if (!here) continue;
         wait(&ctl.s_full[x], s_ph);
         s_ph ^= 1u;
         tc::fence_after_sync();
-        const int seen = limit - b * kBlock;  // of this block's positions
-        const uint32_t* ab = ctl.absent[block & 3];
-        const uint32_t* po = ctl.poison[block & 3];
-        const bool odd = (ab[0] | ab[1] | ab[2] | ab[3] | po[0] | po[1] | po[2] | po[3]) != 0u;
-        const bool plain = __all_sync(0xffffffffu, seen >= kBlock && !odd);
-        auto visible = [&](int q) {  // a bit for each of the positions 32 q .. 32 q + 31
+        const int seen = limit - b * kBlock - 64 * half;  // of this half of the block's positions
+        const uint32_t* ab = ctl.absent[block & 3] + 2 * half;
+        const uint32_t* po = ctl.poison[block & 3] + 2 * half;
+        const bool odd = (ab[0] | ab[1] | po[0] | po[1]) != 0u;
+        const bool plain = __all_sync(0xffffffffu, seen >= 64 && !odd);
+        auto visible = [&](int q) {  // a bit for each of the positions 32 q .. 32 q + 31 of the half
           const int n = seen - 32 * q;
           return (n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u)) & ~ab[q];
         };
-        // 32 positions at a time, each score read once, the next ones on their way; a row whose maximum has passed
-        // its reference by too much (the first block, hardly ever later) is rescaled
-        const float2 rowf2 = make_float2(rowf, rowf);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t v[2][32];
-        tc::ld_x32(s_col, v[0]);
-#pragma unroll 1  // a short loop: four roles share the instruction caches
-        for (int q = 0; q < 4; q += 2) {
+        auto scores = [&](int q, uint32_t (&u)[32]) {
+          tc::ld_x32_sync(s_col + 32 * q, u);
+          if (!plain) {
+            const uint32_t vis = visible(q);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t(&u)[32] = v[h];
-            tc::ld_wait_x32(u);
-            // after the last columns the first ones again, into registers that nothing reads
-            tc::ld_x32(s_col + 32 * ((q + h + 1) & 3), v[h ^ 1]);
-            if (!plain) {
-              const uint32_t vis = visible(q + h);
+            for (int i = 0; i < 32; ++i) u[i] = (vis >> i) & 1u ? u[i] : 0xFF800000u;  // minus infinity
+          }
+        };
+        // the half's maximum; where a row's has passed its reference by too much (the first block, hardly ever
+        // later), both threads of the row take a new one and rescale
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1  // short loops: the roles share the instruction caches
+        for (int q = 0; q < 2; ++q) {
+          uint32_t u[32];
+          scores(q, u);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] = (vis >> i) & 1u ? u[i] : 0xFF800000u;  // minus infinity
-            }
-            float mx[4];
+          for (int i = 0; i < 32; i += 8) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(u[k]), __uint_as_float(u[4 + k]));
-#pragma unroll
-            for (int i = 8; i < 32; i += 8) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(u[i + k])), __uint_as_float(u[i + 4 + k]));
-            }
-            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const float top = most == -INFINITY ? -INFINITY : most * rowf;
-            const bool grow = top > ref + kGrowth || (ref == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float next = fmaxf(ref, top);
-              const float f = ref == -INFINITY ? 0.f : ex2(ref - next);
-              ref = next;
-              l *= f;
-#pragma unroll
-              for (int k = 0; k < 2; ++k) sum[k] = make_float2(sum[k].x * f, sum[k].y * f);
-              rescale<D>(s_col, q + h, f, b > g.b0 ? o_col : 0u);
-            }
-            const float bias = kShift - (ref == -INFINITY ? 0.f : ref);
-            const float2 bias2 = make_float2(bias, bias);
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 x = fma2(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), rowf2, bias2);
-              const float2 e = make_float2(ex2(x.x), ex2(x.y));
-              sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], e);
-              w[i / 2] = pack_half2(e.x, e.y);
-            }
-            tc::st_x16(s_col + 16 * (q + h), w);
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
           }
         }
-        tc::ld_wait_x32(v[0]);
+        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        float top = most == -INFINITY ? -INFINITY : most * rowf;
+        if (any_pair(pair, top > ref + kGrowth || (ref == -INFINITY && top > -INFINITY))) {
+          ctl.top[x][half][row] = top;
+          sync_pair(pair);
+          const float next = fmaxf(ref, fmaxf(top, ctl.top[x][half ^ 1][row]));
+          sync_pair(pair);
+          const float f = ref == -INFINITY ? 0.f : ex2(ref - next);
+          ref = next;
+          l *= f;
+          if (b > g.b0) {  // the last block's product is complete: the scores came after it
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t h[16];
+              tc::ld_x16_sync(o_col + 16 * i, h);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) h[k] = __float_as_uint(__uint_as_float(h[k]) * f);
+              tc::st_x16(o_col + 16 * i, h);
+            }
+          }
+        }
+        // then the probabilities
+        const float bias = kShift - (ref == -INFINITY ? 0.f : ref);
+        const float2 rowf2 = make_float2(rowf, rowf), bias2 = make_float2(bias, bias);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t u[32], w[16];
+          scores(q, u);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = fma2(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), rowf2, bias2);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum[(i / 2) & 1] = add2(sum[(i / 2) & 1], e);
+            w[i / 2] = pack_half2(e.x, e.y);
+          }
+          tc::st_x16(s_col + 16 * q, w);
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (odd) {  // a visible value that is not finite makes the row so
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 2; ++q)
             if (po[q] & visible(q)) l = NAN;
         }
         tc::st_wait();
@@ -401,28 +418,53 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       constexpr size_t kSlot = (size_t)kRows * (D + 2);  // floats: [D / 4][256][4], then (reference, sum) [256]
       float* part = p.part + (size_t)(2 * blockIdx.x + (g.b0 == 0 ? 1 : 0)) * kSlot;
       const int prow = kHalf * x + row;
+      // the output's rows are gathered in the tile's part of the q area, which no MMA reads any more, and leave from
+      // there as whole lines
+      const uint32_t gather = qs + (uint32_t)(x * kOperand);
       auto write = [&](int i, const float (&o)[8], float sum) {  // columns 8 i .. + 7
         const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
         auto two = [&](int a, int b) {
           const __nv_bfloat162 v = __floats2bfloat162_rn(o[a] * inv, o[b] * inv);
           return *reinterpret_cast<const uint32_t*>(&v);
         };
-        *reinterpret_cast<uint4*>(p.out + at + 8 * i) = make_uint4(two(0, 2), two(4, 6), two(1, 3), two(5, 7));
+        tc::sts128(gather + (uint32_t)((i / 8) * kSub) + piece(row, i % 8), two(0, 2), two(4, 6), two(1, 3), two(5, 7));
+      };
+      auto flush = [&] {
+        sync_tile(x);
+        constexpr int kPieces = D / 8, kTurns = 128 * kPieces / 256;
+        const int tt = threadIdx.x & 255, pc = tt % kPieces;
+#pragma unroll
+        for (int j = 0; j < kTurns; ++j) {
+          const int r = j * (256 / kPieces) + tt / kPieces;
+          if (kHalf * x + r < g.rows) {
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(gather + (uint32_t)((pc / 8) * kSub) + piece(r, pc % 8)));
+            *reinterpret_cast<uint4*>(p.out + place(g.row_first + kHalf * x + r) + 8 * pc) = v;
+          }
+        }
+        sync_tile(x);  // the area takes q again
       };
       if (here) {
+        ctl.sum[x][half][row] = l;
+        sync_pair(pair);
+        l = ctl.sum[x][0][row] + ctl.sum[x][1][row];
+        sync_pair(pair);
         wait(&ctl.o_full[x], o_ph);
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
+        for (int j = 0; j < D / 32; ++j) {
+          const int q = half * (D / 32) + j;  // columns 16 q .. + 15
           uint32_t v[16];
-          tc::ld_x16_sync(o_col + 16 * q, v);
+          tc::ld_x16_sync(o_col + 16 * j, v);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(v[8 * i + k]);
             if (whole) {
-              if (live) write(2 * q + i, o, l);
+              write(2 * q + i, o, l);
             } else {
               float4* dst = reinterpret_cast<float4*>(part);
               dst[(4 * q + 2 * i) * kRows + prow] = make_float4(o[0], o[1], o[2], o[3]);
@@ -430,11 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
             }
           }
         }
-        if (!whole) reinterpret_cast<float2*>(part + (size_t)kRows * D)[prow] = make_float2(ref, l);
+        if (!whole && half == 0) reinterpret_cast<float2*>(part + (size_t)kRows * D)[prow] = make_float2(ref, l);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.o_free[x]);
         o_ph ^= 1u;
+        if (whole) flush();
       }
       if (!whole) {
         const int ns = last_cta - first_cta + 1;
@@ -445,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
           if (ctl.last) p.cnt[first_cta] = 0u;
         }
         sync_softmax();
-        if (ctl.last && live) {
+        if (ctl.last && here) {
           __threadfence();
           const float* parts = p.part + (size_t)2 * first_cta * kSlot;
           auto slot = [&](int i) { return parts + (size_t)(i == 0 ? 1 : 2 * i) * kSlot; };
@@ -457,35 +500,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
             sum = fmaf(e.x == -INFINITY ? 0.f : ex2(e.x - top), e.y, sum);
           }
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {  // 32 columns, eight loads in flight
-            float o[4][8] = {};
-#pragma unroll 1
+          for (int j = 0; j < D / 32; ++j) {  // this half's columns, 16 at a time
+            const int q = half * (D / 32) + j;
+            float o[2][8] = {};
+#pragma unroll 2
             for (int i = 0; i < ns; ++i) {
-              const float4* src = reinterpret_cast<const float4*>(slot(i)) + (8 * q) * kRows + prow;
+              const float4* src = reinterpret_cast<const float4*>(slot(i)) + (4 * q) * kRows + prow;
               const float e = __ldcg(reinterpret_cast<const float2*>(slot(i) + (size_t)kRows * D) + prow).x;
-              float4 a[8];
+              float4 a[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) a[k] = __ldcg(src + k * kRows);
+              for (int k = 0; k < 4; ++k) a[k] = __ldcg(src + k * kRows);
               const float f = e == -INFINITY ? 0.f : ex2(e - top);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < 4; ++k) {
                 float* d = o[k / 2] + 4 * (k & 1);
                 d[0] = fmaf(f, a[k].x, d[0]), d[1] = fmaf(f, a[k].y, d[1]);
                 d[2] = fmaf(f, a[k].z, d[2]), d[3] = fmaf(f, a[k].w, d[3]);
               }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) write(4 * q + k, o[k], sum);
+            write(2 * q, o[0], sum);
+            write(2 * q + 1, o[1], sum);
           }
+          flush();
         }
         sync_softmax();
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kMmaWarp) {
     // ------------------------------------------------- codes -> operands
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // Three steps in flight: the page of block i + 2, the codes of block i + 1, block i into shared memory.
-    const int tid = threadIdx.x - 256;  // position within a block
+    const int tid = threadIdx.x - 32 * kExpandWarp;  // position within a block
     struct {
       bool valid, inside;
       int page, slot, h;
@@ -506,65 +551,72 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       ahead.h = g.h;
       ++b;
     };
-    uint4 kn[D / 32], vn[D / 32];
-    uint2 pn = make_uint2(0, 0);
-    bool valid, absent = false;
-    auto load = [&] {
-      valid = ahead.valid;
-      if (!valid) return;
-      const bool there = (unsigned)ahead.page < (unsigned)c.num_pages;
-      absent = ahead.inside && !there;
-      if (absent) kv4::report_bad();
-      pn = make_uint2(0, 0);
+    // a block's keys, then its values; each operand's registers take the next block's codes as soon as they are free
+    struct Block {
+      bool valid, there, absent;
+      const uint8_t* row;  // of the keys
+    } cur, nxt;
+    auto place = [&](Block* n) {
+      n->valid = ahead.valid;
+      if (!n->valid) return;
+      n->there = (unsigned)ahead.page < (unsigned)c.num_pages;
+      n->absent = ahead.inside && !n->there;
+      if (n->absent) kv4::report_bad();
+      n->row = n->there ? c.pages + kv4::block_offset(c, ahead.page, ahead.h) + (size_t)ahead.slot * (D / 2) : nullptr;
+    };
+    const size_t v_off = (size_t)c.page * (D / 2), p_off = (size_t)c.page * D;
+    uint4 kw[D / 32], vw[D / 32];
+    uint2 pair;
+    int slot = 0;
+    auto load = [&](uint4 (&w)[D / 32], const Block& n, size_t off) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) kn[i] = vn[i] = make_uint4(0, 0, 0, 0);
-      if (there) {
-        const uint8_t* blk = c.pages + kv4::block_offset(c, ahead.page, ahead.h);
-        const uint4* kr = reinterpret_cast<const uint4*>(blk + (size_t)ahead.slot * (D / 2));
-        const uint4* vr = reinterpret_cast<const uint4*>(blk + (size_t)(c.page + ahead.slot) * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) kn[i] = __ldg(kr + i), vn[i] = __ldg(vr + i);
-        pn = __ldg(reinterpret_cast<const uint2*>(blk + (size_t)c.page * D + (size_t)ahead.slot * 8));
-      }
+      for (int i = 0; i < D / 32; ++i)
+        w[i] = n.valid && n.there ? __ldg(reinterpret_cast<const uint4*>(n.row + off) + i) : make_uint4(0, 0, 0, 0);
+    };
+    auto load_pair = [&](const Block& n) {  // the scale pairs stand behind the values, 8 bytes a token
+      pair = make_uint2(0, 0);
+      if (n.valid && n.there)
+        pair = __ldg(reinterpret_cast<const uint2*>(n.row - (size_t)slot * (D / 2) + p_off + (size_t)slot * 8));
     };
     look_up();
-    load();
-    if (valid) look_up();
-    for (int block = 0; valid; ++block) {
+    place(&cur);
+    slot = ahead.slot;
+    load(kw, cur, 0);
+    load(vw, cur, v_off);
+    load_pair(cur);
+    if (cur.valid) look_up();
+    for (int block = 0; cur.valid; ++block) {
       const int stage = block & 1;
-      uint4 kw[D / 32], vw[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) kw[i] = kn[i], vw[i] = vn[i];
-      const uint2 pair = pn;
-      const float2 vp = __half22float2(as_half2(pair.y));
+      const uint2 sp = pair;
+      const float2 vp = __half22float2(as_half2(sp.y));
       const bool bad_value = !(fabsf(vp.y) + 15.f * fabsf(vp.x) < 65520.f);  // as fp16, or not a number
-      const uint32_t ab = __ballot_sync(0xffffffffu, absent), po = __ballot_sync(0xffffffffu, bad_value);
-      load();
-      if (valid) look_up();
-#pragma unroll 1  // keys, then values: one copy of the code
-      for (int which = 0; which < 2; ++which) {
-        if (block >= 2)
-          wait(which == 0 ? &ctl.k_empty[stage] : &ctl.v_empty[stage], (uint32_t)(block / 2 - 1) & 1u);
-        if (which == 0) {
-          if (lane == 0) {
-            ctl.absent[block & 3][tid >> 5] = ab;
-            ctl.poison[block & 3][tid >> 5] = po;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) kw[i] = vw[i];
-        }
-        expand<D>((which == 0 ? ks : vs) + (uint32_t)(stage * kOperand), tid, kw,
-                  which == 0 ? pair.x : (bad_value ? 0u : pair.y));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(which == 0 ? &ctl.k_full[stage] : &ctl.v_full[stage]);
+      const uint32_t ab = __ballot_sync(0xffffffffu, cur.absent), po = __ballot_sync(0xffffffffu, bad_value);
+      place(&nxt);
+      slot = ahead.slot;
+      if (block >= 2) wait(&ctl.k_empty[stage], (uint32_t)(block / 2 - 1) & 1u);
+      if (lane == 0) {
+        ctl.absent[block & 3][tid >> 5] = ab;
+        ctl.poison[block & 3][tid >> 5] = po;
       }
+      expand<D>(ks + (uint32_t)(stage * kOperand), tid, kw, sp.x);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl.k_full[stage]);
+      load(kw, nxt, 0);
+      load_pair(nxt);
+      if (nxt.valid) look_up();
+      if (block >= 2) wait(&ctl.v_empty[stage], (uint32_t)(block / 2 - 1) & 1u);
+      expand<D>(vs + (uint32_t)(stage * kOperand), tid, vw, bad_value ? 0u : sp.y);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ctl.v_full[stage]);
+      load(vw, nxt, v_off);
+      cur = nxt;
     }
   } else {
     // ------------------------------------------------------------------ MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == kMmaWarp) {
       // the whole warp in step, one lane of it issuing
       constexpr uint32_t id_s = tc::idesc_f16_f32(kBlock, false), id_o = tc::idesc_f16_f32(D, true);
       const uint32_t lead = lane == 0 ? 1u : 0u;
@@ -588,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
         const uint64_t v = dv + stage * (uint32_t)(kOperand >> 4);
 #pragma unroll
         for (int i = 0; i < kBlock / 16; ++i)
-          tc::mma_f16_ts(tmem + 256u + (uint32_t)(128 * x), tmem + (uint32_t)(128 * x + 8 * i), v + (uint32_t)(i * 128),
+          tc::mma_f16_ts(tmem + 256u + (uint32_t)(128 * x), tmem + (uint32_t)(128 * x + 64 * (i / 4) + 8 * (i % 4)),
+                         v + (uint32_t)(i * 128),
                          id_o, i > 0 ? 1u : more, lead);
       };
       while (walk.next(p, &g)) {
@@ -642,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
   }
   __syncthreads();
-  if (warp == 12) tc::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int D>
