@@ -16,6 +16,10 @@
 //   warp 1     one thread issues the MMAs and commits them to mbarriers;
 //   warps 4-7  read the accumulators (two buffers, so that the next tile's MMAs
 //              run meanwhile), scale and store.
+// Enough tiles for every pair of SMs: pairs of CTAs (cta_group::2) take 256
+// channels by up to 256 tokens, each loading its own 128 channels and half of the
+// tokens, which is 32 KB instead of 48 KB per SM and step (one CTA per tile was
+// held up by these loads: tensor pipe 67 % active).
 // Fewer tiles than SMs: the steps of a tile are dealt to a cluster of 2, 4 or 8
 // CTAs, whose exact int32 partial sums meet in distributed shared memory; each
 // CTA of the cluster finishes a share of the tokens. Integer sums: the result
@@ -47,6 +51,7 @@ constexpr int kSmemTop = 227 * 1024;
 struct Plan {
   int tn, tiles_n, tiles_m, tiles;  // tokens per tile; tiles of channels, of tokens
   int steps, split;                 // of K; CTAs that share a tile
+  int pair;                         // pairs of CTAs, 256 channels per tile
   int stages, stage_bytes, grid;
   uint32_t tmem_cols;
 };
@@ -80,6 +85,7 @@ __device__ __forceinline__ void store_one(const GemmI8Params& p, int m, int n, i
     static_cast<float*>(p.y)[at] = v;
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_i8_kernel(const Args a, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -98,37 +104,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.acc_full[i], 1);
-      mbar_init(&ctl.acc_empty[i], 4);
+      mbar_init(&ctl.acc_empty[i], PAIR ? 8 : 4);
     }
     mbar_init(&ctl.fin, 1);
     ctl.misc[tc::kMiscAbort] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(smem_u32(&ctl.misc[tc::kMiscTmem]), pl.tmem_cols);
-    tc::tmem_relinquish();
+    if constexpr (PAIR) {
+      tc::tmem_alloc_pair(smem_u32(&ctl.misc[tc::kMiscTmem]), pl.tmem_cols);
+    } else {
+      tc::tmem_alloc(smem_u32(&ctl.misc[tc::kMiscTmem]), pl.tmem_cols);
+      tc::tmem_relinquish();
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) {  // both CTAs' barriers exist before either signals the other's
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_wait_acquire();
+  }
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.misc[tc::kMiscTmem], 0);
-  // a tile's CTAs are a cluster of pl.split consecutive ones
-  const int rank = pl.split > 1 ? (int)(blockIdx.x % pl.split) : 0;
-  const int first = (int)blockIdx.x / pl.split, stride = (int)gridDim.x / pl.split;
-  const int k0 = pl.steps * rank / pl.split, k1 = pl.steps * (rank + 1) / pl.split;  // at least one step each
+  // a tile's CTAs are a cluster of consecutive ones: a pair, or pl.split that share K
+  const int ctas = PAIR ? 2 : pl.split, rank = (int)(blockIdx.x % ctas);
+  const int first = (int)blockIdx.x / ctas, stride = (int)gridDim.x / ctas;
+  const int k0 = PAIR ? 0 : pl.steps * rank / pl.split;  // at least one step each
+  const int k1 = PAIR ? pl.steps : pl.steps * (rank + 1) / pl.split;
+  constexpr int kRowsTile = PAIR ? 2 * kRowsA : kRowsA;
+  const int n_off = PAIR ? rank * kRowsA : 0;             // this CTA's channels of a tile
+  const int b_rows = PAIR ? pl.tn / 2 : pl.tn;            // tokens that it loads
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0, issued = 0;
       uint32_t ph = 0;
       for (int tile = first; tile < pl.tiles && !misc[tc::kMiscAbort]; tile += stride) {
-        const int n0 = (tile % pl.tiles_n) * kRowsA, m0 = (tile / pl.tiles_n) * pl.tn;
+        const int n0 = (tile % pl.tiles_n) * kRowsTile + n_off;
+        const int m0 = (tile / pl.tiles_n) * pl.tn + (PAIR ? rank * b_rows : 0);
         for (int k = k0; k < k1; ++k) {
           if (issued >= pl.stages && !tc::tc_wait(&ctl.empty[stage], ph ^ 1u, misc)) break;
           const uint32_t st = ring + (uint32_t)(stage * pl.stage_bytes);
-          mbar_arrive_expect_tx(&ctl.full[stage], (uint32_t)(kBytesA + pl.tn * kStepK));
-          tc::tma_load_2d(st, &map_w, k * kStepK, n0, &ctl.full[stage]);
-          tc::tma_load_2d(st + kBytesA, &map_x, k * kStepK, m0, &ctl.full[stage]);
+          if constexpr (PAIR) {  // both CTAs' loads complete on the even one's barrier
+            const uint32_t bar = map_cluster_rank(smem_u32(&ctl.full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&ctl.full[stage], 2u * (uint32_t)pl.stage_bytes);
+            tc::tma_load_2d_pair(st, &map_w, k * kStepK, n0, bar);
+            tc::tma_load_2d_pair(st + kBytesA, &map_x, k * kStepK, m0, bar);
+          } else {
+            mbar_arrive_expect_tx(&ctl.full[stage], (uint32_t)pl.stage_bytes);
+            tc::tma_load_2d(st, &map_w, k * kStepK, n0, &ctl.full[stage]);
+            tc::tma_load_2d(st + kBytesA, &map_x, k * kStepK, m0, &ctl.full[stage]);
+          }
           ++issued;
           if (++stage == pl.stages) {
             stage = 0;
@@ -136,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (misc[tc::kMiscAbort]) {  // no load may be under way when the CTA ends
+      // no load may be under way when the CTA ends (the odd CTA of a pair waits for the even one below)
+      if (misc[tc::kMiscAbort] && (!PAIR || rank == 0)) {
         for (int i = 0; i < min(issued, pl.stages); ++i) {
           if (--stage < 0) {
             stage = pl.stages - 1;
@@ -146,16 +173,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && (!PAIR || rank == 0)) {
     // the whole warp in step, one lane of it issuing
-    const uint32_t idesc = tc::idesc_i8_s32(pl.tn), lead = lane == 0 ? 1u : 0u;
+    const uint32_t idesc = PAIR ? tc::idesc_i8_s32_pair(pl.tn) : tc::idesc_i8_s32(pl.tn), lead = lane == 0 ? 1u : 0u;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, tc::tc_wait(bar, parity, misc)); };
     int stage = 0, seg = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int tile = first; tile < pl.tiles && ok; tile += stride, ++seg) {
       const int buf = seg & 1;
-      if (seg >= 2) ok = wait(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u);
+      if (seg >= 2)
+        ok = PAIR ? __all_sync(0xffffffffu, tc::tc_wait_cluster(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u, misc))
+                  : wait(&ctl.acc_empty[buf], (uint32_t)(seg / 2 - 1) & 1u);
       tc::fence_after_sync();
       const uint32_t acc = tmem + (uint32_t)(buf * pl.tn);
       for (int k = k0; k < k1 && ok; ++k) {
@@ -165,17 +194,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ad = tc::smem_desc_sw128(st), bd = tc::smem_desc_sw128(st + kBytesA);
 #pragma unroll
         for (int i = 0; i < kStepK / 32; ++i)  // 32 bytes of K: two 16-byte units of the start address
-          tc::mma_i8_lead(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u, ok ? lead : 0u);
-        tc::commit_lead(&ctl.empty[stage], lead);
+          if constexpr (PAIR)
+            tc::mma_i8_pair(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u, ok ? lead : 0u);
+          else
+            tc::mma_i8_lead(acc, ad + 2 * i, bd + 2 * i, idesc, k > k0 || i > 0 ? 1u : 0u, ok ? lead : 0u);
+        PAIR ? tc::commit_pair(&ctl.empty[stage], lead) : tc::commit_lead(&ctl.empty[stage], lead);
         if (++stage == pl.stages) {
           stage = 0;
           ph ^= 1u;
         }
       }
-      tc::commit_lead(&ctl.acc_full[buf], lead);
+      PAIR ? tc::commit_pair(&ctl.acc_full[buf], lead) : tc::commit_lead(&ctl.acc_full[buf], lead);
     }
     // every MMA issued has completed before tensor memory is released
-    tc::commit_lead(&ctl.fin, lead);
+    PAIR ? tc::commit_pair(&ctl.fin, lead) : tc::commit_lead(&ctl.fin, lead);
     mbar_wait_bounded(&ctl.fin, 0u);
   } else if (warp >= 4) {
     const int q4 = warp & 3, et = threadIdx.x - 128;
@@ -183,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg = 0;
     for (int tile = first; tile < pl.tiles; tile += stride, ++seg) {
       const int buf = seg & 1;
-      const int n = (tile % pl.tiles_n) * kRowsA + 32 * q4 + lane, m0 = (tile / pl.tiles_n) * pl.tn;
+      const int n = (tile % pl.tiles_n) * kRowsTile + n_off + 32 * q4 + lane, m0 = (tile / pl.tiles_n) * pl.tn;
       const int cols = min(pl.tn, p.m - m0);
       float* sx = ctl.sx[buf];
       for (int i = et; i < cols; i += 128) sx[i] = __ldg(p.xscale + m0 + i);
@@ -195,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < pl.tn; c += 16) {
         uint32_t v[16];
         tc::ld_x16_sync(acc + (uint32_t)c, v);
-        if (pl.split > 1) {  // [token][channel] at the ring's start: the loads are all in, and read
+        if (!PAIR && pl.split > 1) {  // [token][channel] at the ring's start: the loads are all in, and read
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + (uint32_t)((c + i) * kRowsA + 32 * q4 + lane) * 4u),
@@ -209,11 +241,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&ctl.acc_empty[buf]);
+      if (lane == 0) {
+        if constexpr (PAIR)
+          tc::mbar_arrive_cluster(map_cluster_rank(smem_u32(&ctl.acc_empty[buf]), 0));
+        else
+          tc::mbar_arrive(&ctl.acc_empty[buf]);
+      }
     }
   }
   __syncthreads();
-  if (pl.split > 1) {
+  if constexpr (PAIR) {  // neither CTA's shared memory, barriers or tensor memory go before the other is done
+    cluster_arrive_relaxed();
+    cluster_wait_acquire();
+  }
+  if (!PAIR && pl.split > 1) {
     // the cluster's partial sums, a share of the tokens per CTA
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     cluster_wait_acquire();
@@ -234,25 +275,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_arrive_relaxed();  // a CTA's shared memory stays until its peers have read it
     cluster_wait_acquire();
   }
-  if (warp == 1) tc::tmem_dealloc(tmem, pl.tmem_cols);
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tc::tmem_dealloc_pair(tmem, pl.tmem_cols);
+    else
+      tc::tmem_dealloc(tmem, pl.tmem_cols);
+  }
 }
 
-// Tokens per tile: the fewest tiles of up to 256, of equal size. Fewer tiles
-// than SMs: split K over a cluster, as long as every CTA keeps four steps.
+// Tokens per tile: the fewest tiles of up to 256, of equal size. Pairs of CTAs
+// from one 256-channel tile per pair of SMs on. Fewer tiles than SMs: split K over
+// a cluster, as long as every CTA keeps four steps.
 Plan make_plan(int m, int n, int k, int sms) {
   Plan pl{};
   pl.tiles_m = (m + 255) / 256;
-  pl.tn = ((m + pl.tiles_m - 1) / pl.tiles_m + 15) / 16 * 16;
+  const long long pair_tiles = (long long)((n + 2 * kRowsA - 1) / (2 * kRowsA)) * pl.tiles_m;
+  pl.pair = m > 64 && pair_tiles >= sms / 2;
+  const int unit = pl.pair ? 32 : 16, rows = pl.pair ? 2 * kRowsA : kRowsA;
+  pl.tn = ((m + pl.tiles_m - 1) / pl.tiles_m + unit - 1) / unit * unit;
   pl.tiles_m = (m + pl.tn - 1) / pl.tn;
-  pl.tiles_n = (n + kRowsA - 1) / kRowsA;
+  pl.tiles_n = (n + rows - 1) / rows;
   pl.steps = (k + kStepK - 1) / kStepK;
   const long long tiles = (long long)pl.tiles_n * pl.tiles_m;
   pl.tiles = (int)std::min(tiles, 0x7FFFFFFFll);
   pl.split = 1;
-  while (pl.split < kMaxSplit && tiles * pl.split * 2 <= sms && pl.steps >= pl.split * 2 * 4) pl.split *= 2;
-  pl.stage_bytes = kBytesA + pl.tn * kStepK;
+  while (!pl.pair && pl.split < kMaxSplit && tiles * pl.split * 2 <= sms && pl.steps >= pl.split * 2 * 4) pl.split *= 2;
+  pl.stage_bytes = kBytesA + (pl.pair ? pl.tn / 2 : pl.tn) * kStepK;
   pl.stages = std::min(kMaxStages, (kSmemTop - 1024 - kCtlBytes) / pl.stage_bytes);
-  pl.grid = (int)std::min<long long>(tiles * pl.split, pl.split > 1 ? tiles * pl.split : sms);
+  pl.grid = pl.pair ? 2 * (int)std::min<long long>(tiles, sms / 2)
+                    : (int)std::min<long long>(tiles * pl.split, pl.split > 1 ? tiles * pl.split : sms);
   pl.tmem_cols = 32;
   while (pl.tmem_cols < 2u * (uint32_t)pl.tn) pl.tmem_cols *= 2;
   return pl;
@@ -289,9 +340,12 @@ bool encode(CUtensorMap* map, const int8_t* base, int k, int rows, int64_t ld, i
 int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
   Args a{p, make_plan(p.m, p.n, p.k, sms)};
   CUtensorMap mw, mx;
-  if (!encode(&mw, p.w, p.k, p.n, p.ldw, kRowsA) || !encode(&mx, p.x, p.k, p.m, p.ldx, a.pl.tn)) return -1;
-  const int bytes = kSmemTop;
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (!encode(&mw, p.w, p.k, p.n, p.ldw, kRowsA) ||
+      !encode(&mx, p.x, p.k, p.m, p.ldx, a.pl.pair ? a.pl.tn / 2 : a.pl.tn))
+    return -1;
+  auto kernel = a.pl.pair ? gemm_i8_kernel<true> : gemm_i8_kernel<false>;
+  const int bytes = kSmemTop, cluster = a.pl.pair ? 2 : a.pl.split;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.pl.grid);
@@ -299,13 +353,13 @@ int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
   cfg.dynamicSmemBytes = (size_t)bytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
-  if (a.pl.split > 1) {
+  if (cluster > 1) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)a.pl.split, 1, 1};
+    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, gemm_i8_kernel, a, mw, mx);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, mw, mx);
   return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 

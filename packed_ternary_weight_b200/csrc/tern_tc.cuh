@@ -222,6 +222,55 @@ __device__ __forceinline__ void ld_x4_sync(uint32_t taddr, uint32_t (&v)[4]) {
       : "memory");
 }
 
+// ---- pairs of CTAs (cta_group::2): one MMA over both CTAs' shared memory, M =
+// 256 rows of which each CTA holds 128, accumulators in both tensor memories;
+// issued by the CTA of even rank. Both CTAs execute allocation and release.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// As idesc_i8_s32 with M = 256; N a multiple of 32.
+__host__ __device__ constexpr uint32_t idesc_i8_s32_pair(int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// commit_lead on the barrier at this place in both CTAs of the pair.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+// tma_load_2d into this CTA, completing on a barrier of either CTA of the pair
+// (its address in the cluster's window).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst_smem, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst_smem),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Words after the mbarriers of a tensor-core kernel: the tensor-memory base
 // address, the abort flag of its bounded waits, the last-arrival flag.
 constexpr int kMiscTmem = 0, kMiscAbort = 1, kMiscLast = 2;
@@ -269,6 +318,22 @@ __device__ __forceinline__ bool tc_wait_many(uint64_t* bar, uint32_t parity, vol
     __nanosleep(64);
     if (mbar_test(bar, parity)) return true;
     if ((it & 63u) == 0u) {
+      if (misc[kMiscAbort]) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(&g_dev_error, TERN_DEVERR_TIMEOUT);
+        misc[kMiscAbort] = 1u;
+        return false;
+      }
+    }
+  }
+}
+
+// tc_wait for phases that the other CTA's threads complete.
+__device__ __forceinline__ bool tc_wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* misc) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait<true>(bar, parity)) return true;
+    if ((it & 255u) == 0u || global_timer_ns() - t0 > kWaitLimitNs) {
       if (misc[kMiscAbort]) return false;
       if (global_timer_ns() - t0 > kWaitLimitNs) {
         atomicOr(&g_dev_error, TERN_DEVERR_TIMEOUT);

@@ -76,6 +76,14 @@ def test_larger(tern, m, n, k):
     check(tern, m, n, k, torch.bfloat16, seed=m)
 
 
+@pytest.mark.parametrize("m,n,k", [(65, 19000, 64), (96, 18945, 1), (257, 9600, 272), (300, 9473, 100), (512, 9500, 129), (513, 6400, 640),
+                                   (1023, 5000, 500), (4096, 1300, 333)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_many_tiles(tern, m, n, k, out):
+    # more tiles than multiprocessors: several per CTA, odd ends on every side
+    check(tern, m, n, k, out, pad=1, ypad=2, seed=m)
+
+
 def test_weights_quantised_per_channel(tern):
     # tern_quantize_act gives the weights and their scales
     g = torch.Generator().manual_seed(3)
