@@ -20,7 +20,7 @@
 // channels by up to 256 tokens, each loading its own 128 channels and half of the
 // tokens, which is 32 KB instead of 48 KB per SM and step (one CTA per tile was
 // held up by these loads: tensor pipe 67 % active).
-// Fewer tiles than SMs: the steps of a tile are dealt to a cluster of 2, 4 or 8
+// Fewer tiles than SMs: the steps of a tile are dealt to a cluster of up to eight
 // CTAs, whose exact int32 partial sums meet in distributed shared memory; each
 // CTA of the cluster finishes a share of the tokens. Integer sums: the result
 // does not depend on the split.
@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "tern_tc.cuh"
 
@@ -46,6 +47,7 @@ constexpr int kStepK = 128;               // bytes of K per step
 constexpr int kBytesA = kRowsA * kStepK;  // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;
+constexpr int kMinSteps = 4;              // of K for each CTA of a split tile
 constexpr int kSmemTop = 227 * 1024;
 
 struct Plan {
@@ -70,9 +72,12 @@ constexpr int kCtlBytes = 3 * 1024;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
 
 __device__ __forceinline__ void named_sync_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ uint32_t ld_dsmem(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_dsmem(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -109,6 +114,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl.fin, 1);
     ctl.misc[tc::kMiscAbort] = 0;
     fence_mbar_init();
+  }
+  if (warp == 2 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -260,15 +269,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait_acquire();
     const int n0 = (first % pl.tiles_n) * kRowsA, m0 = (first / pl.tiles_n) * pl.tn;
     const int cols = min(pl.tn, p.m - m0);
-    const int n = n0 + (int)(threadIdx.x & 127);
+    // four channels of a token per thread and turn, every CTA's sums in one go
+    const int n = n0 + 4 * (int)(threadIdx.x & 31);
     if (n < p.n) {
-      const float sw = __ldg(p.wscale + n);
-      for (int c = rank + pl.split * (int)(threadIdx.x >> 7); c < cols; c += 2 * pl.split) {
-        const uint32_t at = ring + (uint32_t)(c * kRowsA + (int)(threadIdx.x & 127)) * 4u;
-        int acc = 0;
-#pragma unroll 8
-        for (int r = 0; r < pl.split; ++r) acc += (int)ld_dsmem(map_cluster_rank(at, (uint32_t)r));
-        store_one(p, m0 + c, n, acc, sw, __ldg(p.xscale + m0 + c));
+      float sw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[i] = n + i < p.n ? __ldg(p.wscale + n + i) : 0.f;
+      for (int c = rank + pl.split * (int)(threadIdx.x >> 5); c < cols; c += 8 * pl.split) {
+        const uint32_t at = ring + (uint32_t)(c * kRowsA + 4 * (int)(threadIdx.x & 31)) * 4u;
+        const float sx = __ldg(p.xscale + m0 + c);
+        int4 v[kMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          v[r] = r < pl.split ? ld_dsmem(map_cluster_rank(at, (uint32_t)r)) : make_int4(0, 0, 0, 0);
+        int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) acc[0] += v[r].x, acc[1] += v[r].y, acc[2] += v[r].z, acc[3] += v[r].w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.n) store_one(p, m0 + c, n + i, acc[i], sw[i], sx);
       }
     }
     __syncwarp();
@@ -283,9 +302,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Clusters of each size that the device holds at once (whole clusters fit into a
+// group of multiprocessors: 20 clusters of seven took two waves of 16, 8.7 us for 1
+// x 2560 x 2560, where 20 of five took one, 5.1 us). Asked once per device.
+const int* resident_clusters(int sms) {
+  constexpr int kDevices = 64;
+  static int table[kDevices][kMaxSplit + 1];
+  static std::mutex lock;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) {
+    cudaGetLastError();
+    dev = 0;
+  }
+  const std::lock_guard<std::mutex> hold(lock);
+  int* t = table[dev];
+  if (t[1] == 0) {
+    for (int s = 2; s <= kMaxSplit; ++s) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)(s * (sms / s)));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmemTop;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {(unsigned)s, 1, 1};
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaFuncSetAttribute(gemm_i8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTop) !=
+              cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&n, gemm_i8_kernel<false>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      t[s] = n;
+    }
+    t[1] = sms;
+  }
+  return t;
+}
+
 // Tokens per tile: the fewest tiles of up to 256, of equal size. Pairs of CTAs
 // from one 256-channel tile per pair of SMs on. Fewer tiles than SMs: split K over
-// a cluster, as long as every CTA keeps four steps.
+// a cluster, as long as every CTA keeps four steps; of the cluster sizes the one
+// with the least steps in a row, where meeting costs about four.
 Plan make_plan(int m, int n, int k, int sms) {
   Plan pl{};
   pl.tiles_m = (m + 255) / 256;
@@ -299,7 +358,15 @@ Plan make_plan(int m, int n, int k, int sms) {
   const long long tiles = (long long)pl.tiles_n * pl.tiles_m;
   pl.tiles = (int)std::min(tiles, 0x7FFFFFFFll);
   pl.split = 1;
-  while (!pl.pair && pl.split < kMaxSplit && tiles * pl.split * 2 <= sms && pl.steps >= pl.split * 2 * 4) pl.split *= 2;
+  if (!pl.pair && tiles <= sms / 2) {
+    const int* fit = resident_clusters(sms);
+    long long best = pl.steps;
+    for (int s = 2; s <= kMaxSplit && s * kMinSteps <= pl.steps; ++s) {
+      if (fit[s] < 1) continue;
+      const long long cost = (tiles + fit[s] - 1) / fit[s] * ((pl.steps + s - 1) / s + kMinSteps);
+      if (cost < best) best = cost, pl.split = s;
+    }
+  }
   pl.stage_bytes = kBytesA + (pl.pair ? pl.tn / 2 : pl.tn) * kStepK;
   pl.stages = std::min(kMaxStages, (kSmemTop - 1024 - kCtlBytes) / pl.stage_bytes);
   pl.grid = pl.pair ? 2 * (int)std::min<long long>(tiles, sms / 2)
