@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -487,7 +488,35 @@ tern_status run_single(const tern_desc* desc, const Layout& L, const void* d_pac
 
 }  // namespace
 
-int sm_count() { return device_sms(); }
+int sm_count() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return device_sms();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) known[dev].store(n = device_sms(), std::memory_order_relaxed);
+  return n;
+}
+
+int allow_smem(const void* kernel, int bytes) {
+  constexpr int kDevices = 64, kKernels = 32;
+  static std::atomic<const void*> known[kDevices][kKernels];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  if (dev < 0 || dev >= kDevices) return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (int i = 0; i < kKernels; ++i) {
+    const void* k = known[dev][i].load(std::memory_order_acquire);
+    if (k == kernel) return 0;
+    if (k != nullptr) continue;
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (set != cudaSuccess) return (int)set;
+    const void* none = nullptr;
+    known[dev][i].compare_exchange_strong(none, kernel);  // lost: set again by the next call, harmless
+    return 0;
+  }
+  return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 }  // namespace tern
 

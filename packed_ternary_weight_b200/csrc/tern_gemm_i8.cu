@@ -412,8 +412,8 @@ int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
     return -1;
   auto kernel = a.pl.pair ? gemm_i8_kernel<true> : gemm_i8_kernel<false>;
   const int bytes = kSmemTop, cluster = a.pl.pair ? 2 : a.pl.split;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return (int)e;
+  const int rc = allow_smem(reinterpret_cast<const void*>(kernel), bytes);
+  if (rc != 0) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.pl.grid);
   cfg.blockDim = dim3(kThreads);
@@ -426,7 +426,7 @@ int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  e = cudaLaunchKernelEx(&cfg, kernel, a, mw, mx);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, mw, mx);
   return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
 }
 

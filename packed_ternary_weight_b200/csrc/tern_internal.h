@@ -396,6 +396,8 @@ int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream);
 int read_clear_dev_error_gemm_i8(void* stream, unsigned* out);
 
 int sm_count();  // multiprocessors of the current device
+// cudaFuncSetAttribute of the dynamic shared memory, once per kernel and device; a cudaError_t
+int allow_smem(const void* kernel, int bytes);
 
 // Shared-memory bytes a 2-bit GEMV CTA needs for these parameters.
 size_t gemv2_smem_bytes(const Gemv2Params& p, int xmode);

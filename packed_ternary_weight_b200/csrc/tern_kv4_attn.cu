@@ -591,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
 template <int D, int NT>
 int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
   constexpr int bytes = (int)sizeof(Shared<D, NT>);
-  const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return (int)e;
+  const int rc = allow_smem(reinterpret_cast<const void*>(attn_kernel<D, NT>), bytes);
+  if (rc != 0) return rc;
   attn_kernel<D, NT><<<ctas, kThreads, bytes, s>>>(p);
   return (int)cudaGetLastError();
 }

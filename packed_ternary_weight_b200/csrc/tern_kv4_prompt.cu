@@ -701,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
 template <int D>
 int launch_dim(const Kv4PromptParams& p, int ctas, cudaStream_t s) {
   constexpr int bytes = 1024 + kCtlBytes + 6 * (D / 64) * kSub;
-  const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return (int)e;
+  const int rc = allow_smem(reinterpret_cast<const void*>(prompt_kernel<D>), bytes);
+  if (rc != 0) return rc;
   prompt_kernel<D><<<ctas, kThreads, bytes, s>>>(p);
   return (int)cudaGetLastError();
 }

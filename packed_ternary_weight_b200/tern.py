@@ -284,13 +284,16 @@ def fit_bt(w, depth: int, codebook, trits, idx, stream=None):
 
 
 _torch = None
+_OUT_TYPE: dict = {}
 
 
 def _import_torch():
     """torch, imported on first use (packing needs none); its types as TERN_OUT_*."""
-    global _torch, _OUT_TYPE
+    global _torch, _current_stream
     import torch
-    _OUT_TYPE = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+    _OUT_TYPE.update({torch.float32: OUT_F32, torch.bfloat16: OUT_BF16})
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)  # the handle alone costs a tenth of the object
     _torch = torch
     return torch
 
@@ -305,14 +308,15 @@ def _type(t, what: str) -> int:
     return o if o is not None else _bad(f"{what}: {t.dtype} is neither float32 nor bfloat16")
 
 
-def _rows(t, m: int, k: int, what: str) -> int:
-    """Row stride of a tensor [m][k] whose rows are contiguous."""
-    if t.dim() != 2 or tuple(t.shape) != (m, k):
+def _rows(t, shape, what: str) -> int:
+    """Row stride of a tensor of shape (m, k) whose rows are contiguous."""
+    if t.shape != shape or len(shape) != 2:
         _bad(what)
     ld, one = t.stride()
+    m, k = shape
     if one != 1 and k > 1:
         _bad(what)
-    return ld if m > 1 and ld > k else k if m <= 1 else ld
+    return ld if m > 1 else k
 
 
 def _vector(t, n: int, dtype, what: str):
@@ -328,7 +332,7 @@ def _launch(dev: int, stream, what: str, fn, *args):
     if dev != cuda.current_device():
         with cuda.device(dev):
             return _launch(dev, stream, what, fn, *args)
-    code = fn(*args, cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+    code = fn(*args, _current_stream(dev) if stream is None else _stream(stream))
     if code != OK:
         raise TernError(code, what)
 
@@ -339,7 +343,8 @@ def norm_quantize(mode: int, x, r, gain, eps: float, sum, xq, xscale, stream=Non
     [m][k], xscale float32 [m]."""
     what = "tern_norm_quantize"
     t = _torch or _import_torch()
-    m, k = x.shape
+    shape = x.shape
+    m, k = shape
     dev = x.get_device()
     _vector(gain, k, t.float32, "tern_norm_quantize: gain")
     _vector(xscale, m, t.float32, "tern_norm_quantize: xscale")
@@ -349,20 +354,20 @@ def norm_quantize(mode: int, x, r, gain, eps: float, sum, xq, xscale, stream=Non
     if mode != NORM_PLAIN:
         if r is None:
             _bad(f"{what}: r is missing")
-        rt, rp, ldr = _type(r, what), r.data_ptr(), _rows(r, m, k, "tern_norm_quantize: r")
+        rt, rp, ldr = _type(r, what), r.data_ptr(), _rows(r, shape, "tern_norm_quantize: r")
         if r.get_device() != dev:
             _bad(f"{what}: tensors on several devices")
     if mode == NORM_ADD:
         if sum is None or sum.dtype is not r.dtype:
             _bad(f"{what}: sum has r's type")
-        sp, lds = sum.data_ptr(), _rows(sum, m, k, "tern_norm_quantize: sum")
+        sp, lds = sum.data_ptr(), _rows(sum, shape, "tern_norm_quantize: sum")
         if sum.get_device() != dev:
             _bad(f"{what}: tensors on several devices")
     if gain.get_device() != dev or xq.get_device() != dev or xscale.get_device() != dev:
         _bad(f"{what}: tensors on several devices")
     _launch(dev, stream, what, lib.tern_norm_quantize, mode, m, k, _type(x, what), x.data_ptr(),
-            _rows(x, m, k, "tern_norm_quantize: x"), rt, rp, ldr, gain.data_ptr(), eps, sp, lds, xq.data_ptr(),
-            _rows(xq, m, k, "tern_norm_quantize: xq"), xscale.data_ptr())
+            _rows(x, shape, "tern_norm_quantize: x"), rt, rp, ldr, gain.data_ptr(), eps, sp, lds, xq.data_ptr(),
+            _rows(xq, shape, "tern_norm_quantize: xq"), xscale.data_ptr())
 
 
 def gemm_i8(x, xscale, w, wscale, y, stream=None):
@@ -379,13 +384,13 @@ def gemm_i8(x, xscale, w, wscale, y, stream=None):
     dev = x.get_device()
     if w.get_device() != dev or xscale.get_device() != dev or wscale.get_device() != dev or y.get_device() != dev:
         _bad(f"{what}: tensors on several devices")
-    ldx, ldw = _rows(x, m, k, "tern_gemm_i8: x"), _rows(w, n, k, "tern_gemm_i8: w")
+    ldx, ldw = _rows(x, (m, k), "tern_gemm_i8: x"), _rows(w, (n, k), "tern_gemm_i8: w")
     if m <= 1:
         ldx = (ldx + 15) & ~15  # the stride of a single row is free
     if n <= 1:
         ldw = (ldw + 15) & ~15
     _launch(dev, stream, what, lib.tern_gemm_i8, m, n, k, x.data_ptr(), ldx, xscale.data_ptr(), w.data_ptr(), ldw,
-            wscale.data_ptr(), _type(y, what), y.data_ptr(), _rows(y, m, n, "tern_gemm_i8: y"))
+            wscale.data_ptr(), _type(y, what), y.data_ptr(), _rows(y, (m, n), "tern_gemm_i8: y"))
 
 
 class KV4Batch:
@@ -437,7 +442,7 @@ class KV4Cache:
         """Row stride of a token buffer [tokens][heads * head_dim] on the cache's device."""
         if t.get_device() != self.dev:
             _bad(f"{what}: tensors on several devices")
-        return _rows(t, tokens, heads * self.head_dim, what)
+        return _rows(t, (tokens, heads * self.head_dim), what)
 
     def append(self, batch: KV4Batch, q, k, v, rope, q_out, stream=None):
         """Rotate q and k by position, store k and v. q [tokens][heads * head_dim] and q_out (bfloat16, contiguous)
