@@ -63,18 +63,35 @@ template <int WARPS, typename Weight>
 __device__ __forceinline__ bool find_share(int seqs, long long min_share, Weight weight, ShareScratch<WARPS>& sm,
                                            Share* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long total = 0;
+  // sums over the CTA of v, of this thread's and of the earlier threads' v
+  auto scan = [&](long long v, long long* incl) {
+    *incl = v;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, *incl, k);
+      if (lane >= k) *incl += u;
+    }
+    if (lane == 31) sm.scan[warp] = *incl;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      if (k < warp) *incl += sm.scan[k];
+      all += sm.scan[k];
+    }
+    return all;
+  };
+  // up to as many sequences as threads: one of them each, scanned once; more: their sum first
+  const bool one_pass = seqs <= 32 * WARPS;
+  long long total = 0, w = 0, incl = 0;
   if (seqs == 1) {
     total = weight(0, blockIdx.x == 0 && threadIdx.x == 0);
+  } else if (one_pass) {
+    w = (int)threadIdx.x < seqs ? weight(threadIdx.x, blockIdx.x == 0) : 0;
+    total = scan(w, &incl);
   } else {
-    long long v = 0;
-    for (int i = threadIdx.x; i < seqs; i += 32 * WARPS) v += weight(i, blockIdx.x == 0);
-#pragma unroll
-    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    if (lane == 0) sm.scan[warp] = v;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) total += sm.scan[i];
+    for (int i = threadIdx.x; i < seqs; i += 32 * WARPS) w += weight(i, blockIdx.x == 0);
+    total = scan(w, &incl);
     __syncthreads();
   }
   const long long ctas = min((long long)gridDim.x, max(min(total, 1ll), total / min_share));
@@ -89,25 +106,18 @@ __device__ __forceinline__ bool find_share(int seqs, long long min_share, Weight
   long long before = 0;
   for (int base = 0; base < seqs; base += 32 * WARPS) {
     const int i = base + threadIdx.x;
-    const long long w = i < seqs ? weight(i, false) : 0;
-    long long incl = w;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, k);
-      if (lane >= k) incl += v;
-    }
-    if (lane == 31) sm.scan[warp] = incl;
     if (threadIdx.x == 0) sm.found = -1;
-    __syncthreads();
-    long long pre = before;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-      if (k < warp) pre += sm.scan[k];
-      before += sm.scan[k];
+    if (one_pass) {
+      __syncthreads();
+    } else {
+      w = i < seqs ? weight(i, false) : 0;
+      const long long all = scan(w, &incl);
+      incl += before;
+      before += all;
     }
-    if (out->at >= pre + incl - w && out->at < pre + incl) {
+    if (out->at >= incl - w && out->at < incl) {
       sm.found = i;
-      sm.off = out->at - (pre + incl - w);
+      sm.off = out->at - (incl - w);
     }
     __syncthreads();
     if (sm.found >= 0) break;

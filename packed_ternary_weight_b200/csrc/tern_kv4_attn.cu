@@ -140,14 +140,17 @@ __device__ __forceinline__ long long rounds_of(const Kv4AttnParams& p, const kv4
   return q.ok && q.n * p.group <= p.max_rows ? (long long)p.c.kv_heads * *tiles * *rounds : 0;
 }
 
-__device__ __forceinline__ void store_row(const Kv4AttnParams& p, const kv4::Seq& q, int D, int h, int row, int d,
+// The exchanges hold a row's dimensions in the order that the accumulators have
+// them, two at a time: place 16 i + 2 r + e is dimension r D/8 + 2 i + e (lanes then
+// write without bank conflicts). store_row puts four places back.
+template <int D>
+__device__ __forceinline__ void store_row(const Kv4AttnParams& p, const kv4::Seq& q, int h, int row, int place,
                                           const float (&o)[4], float l) {
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);  // no position: zero; NaN stays
-  const int tok = row / p.group;
-  __nv_bfloat162 v[2] = {__floats2bfloat162_rn(o[0] * inv, o[1] * inv), __floats2bfloat162_rn(o[2] * inv, o[3] * inv)};
-  *reinterpret_cast<uint2*>(
-      p.out + ((size_t)(q.row0 + tok) * p.c.heads + (size_t)h * p.group + (row - tok * p.group)) * D + d) =
-      *reinterpret_cast<const uint2*>(v);
+  const int tok = row / p.group, i = place >> 4, r = (place & 15) >> 1;
+  uint16_t* out = p.out + ((size_t)(q.row0 + tok) * p.c.heads + (size_t)h * p.group + (row - tok * p.group)) * D;
+  *reinterpret_cast<__nv_bfloat162*>(out + r * (D / 8) + 2 * i) = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+  *reinterpret_cast<__nv_bfloat162*>(out + (r + 1) * (D / 8) + 2 * i) = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
 }
 
 // A warp's softmax state and queries: NT tiles of eight rows; the lane holds
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
       if (r == 0) sm.m[warp][n] = S.m[j][e], sm.l[warp][n] = S.l[j][e];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<float2*>(&sm.o[warp][n][r * (D / 8) + 2 * i]) =
+        *reinterpret_cast<float2*>(&sm.o[warp][n][16 * i + 2 * r]) =
             make_float2(fmaf(S.o[j][i][e], back_even, S.corr[j][e]), fmaf(S.o[j][i][2 + e], back_odd, S.corr[j][e]));
     }
   }
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
       v[3] = fmaf(f, x.w, v[3]);
     }
     if (whole) {
-      store_row(p, q, D, h, row_first + n, d, v, sum);
+      store_row<D>(p, q, h, row_first + n, d, v, sum);
     } else {
       *reinterpret_cast<float4*>(part + n * D + d) = make_float4(v[0], v[1], v[2], v[3]);
       if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * n) = make_float2(mx, sum);
@@ -531,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
   if (!whole) {
     // the last CTA of the tile to arrive joins its parts
     const int ns = last_cta - first_cta + 1;
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
+      __threadfence();  // of the whole CTA's stores, which the barrier has put before it
       sm.last = atomicAdd(p.cnt + first_cta, 1u) == (unsigned)(ns - 1);
       if (sm.last) p.cnt[first_cta] = 0u;
+      __threadfence();
     }
     __syncthreads();
     if (sm.last) {
-      __threadfence();
       const float* parts = p.part + (size_t)2 * first_cta * kSlot;
       auto slot = [&](int i) { return parts + (size_t)(i == 0 ? 1 : 2 * i) * kSlot; };
       for (int i = threadIdx.x; i < ns * R; i += kThreads)
@@ -562,12 +565,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
         if (lane == 0) sm.sum[n] = sum;
       }
       __syncthreads();
-      for (int item = threadIdx.x; item < R * (D / 4); item += kThreads) {
-        const int n = item / (D / 4), d = (item - n * (D / 4)) * 4;
-        if (row_first + n >= rows) continue;
+      // `fan` neighbouring threads share an item's parts where the tile has fewer rows than threads for them
+      const int live = min(R, rows - row_first), items = live * (D / 4);
+      int fan = 1;
+      while (fan < 8 && 2 * fan * items <= kThreads) fan *= 2;
+      for (int base = 0; base < items * fan; base += kThreads) {  // whole warps
+        const int w = base + (int)threadIdx.x, item = w / fan, part0 = w % fan;
+        const bool in = item < items;
+        const int n = in ? item / (D / 4) : 0, d = in ? (item - n * (D / 4)) * 4 : 0;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int i = 0; i < ns; ++i) {
+#pragma unroll 10
+        for (int i = part0; i < ns; i += fan) {
           const float4 x = __ldcg(reinterpret_cast<const float4*>(slot(i) + n * D + d));
           const float f = sm.ml[i][n].x;
           v[0] = fmaf(f, x.x, v[0]);
@@ -575,7 +583,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
           v[2] = fmaf(f, x.z, v[2]);
           v[3] = fmaf(f, x.w, v[3]);
         }
-        store_row(p, q, D, h, row_first + n, d, v, sm.sum[n]);
+        for (int k = 1; k < fan; k <<= 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], k);
+        }
+        if (in && part0 == 0) store_row<D>(p, q, h, row_first + n, d, v, sm.sum[n]);
       }
     }
   }

@@ -481,15 +481,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       }
       if (!whole) {
         const int ns = last_cta - first_cta + 1;
-        __threadfence();
         sync_softmax();
         if (threadIdx.x == 0) {
+          __threadfence();  // of all these warps' stores, which the barrier has put before it
           ctl.last = atomicAdd(p.cnt + first_cta, 1u) == (unsigned)(ns - 1);
           if (ctl.last) p.cnt[first_cta] = 0u;
+          __threadfence();
         }
         sync_softmax();
         if (ctl.last && here) {
-          __threadfence();
           const float* parts = p.part + (size_t)2 * first_cta * kSlot;
           auto slot = [&](int i) { return parts + (size_t)(i == 0 ? 1 : 2 * i) * kSlot; };
           float top = -INFINITY, sum = 0.f;
