@@ -324,6 +324,121 @@ def test_peaked_and_flat_scores(tern):
     run_attention(tern, b, 8, scale=-0.05)
 
 
+def test_prompts_peaked_flat_and_negative(tern):
+    b = util().Batch([40, 33], [300, 33], 1, 128, 32, seed=22)
+    b.fill_values(spread=2.0)
+    run_attention(tern, b, 4, spread=10.0)
+    run_attention(tern, b, 4, scale=0.0)
+    run_attention(tern, b, 4, scale=-0.05)
+    run_attention(tern, b, 4, spread=1e-6, scale=3.0)
+    run_attention(tern, b, 4, spread=1e9, scale=1e-9)
+
+
+def test_prompt_rows_of_very_different_size(tern):
+    # one huge query row must not cost the others their bits
+    u = util()
+    b = u.Batch([30], [200], 1, 64, 16, seed=23)
+    b.fill_values()
+    g = np.random.default_rng(5)
+    q = g.standard_normal((30, 4 * 64))
+    q[7, 64:128] *= 1e12
+    q[9, :64] *= 1e-12
+    run_attention(tern, b, 4, q=u.bf16_dev(q))
+    b = u.Batch([3], [200], 1, 64, 16, seed=24)
+    b.fill_values()
+    run_attention(tern, b, 4, q=u.bf16_dev(q[6:9]))
+
+
+def test_maxima_that_keep_growing(tern):
+    # keys ordered so that every block passes the running maximum by more than any threshold: the accumulators are
+    # rescaled again and again
+    u = util()
+    for new, heads in ((1, 4), (40, 4)):
+        b = u.Batch([new], [700], 1, 64, 16, seed=25)
+        c = b.oracle_cache()
+        for j in range(700):
+            x = np.full(64, 0.02 * j, np.float32)
+            x[::2] += 0.01
+            for w in range(2):
+                q, s, m = prompt.quantize4((x if w == 0 else b.g.standard_normal(64).astype(np.float32))[None])
+                c.put(int(b.table[0, j // 16]), j % 16, 0, w, q[0], s[0], m[0])
+        run_attention(tern, b, heads, scale=1.0, q=u.bf16_dev(np.abs(b.g.standard_normal((new, heads * 64))) + 0.5))
+
+
+@pytest.mark.parametrize("new,heads", [(5, 2), (60, 2)])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_values_that_are_not_numbers_stay_behind_the_mask(tern, new, heads, which, bad):
+    # a position whose key or value scale is not finite: rows that do not see it are as without it; rows that do are
+    # not numbers (its keys being infinite may also leave no finite score)
+    u = util()
+    b = u.Batch([new], [400], 1, 64, 16, seed=26)
+    b.fill_values()
+    q, want = run_attention(tern, b, heads)
+    at = 400 - new + new // 2
+    codes, s, m = b.oracle_cache().get(int(b.table[0, at // 16]), at % 16, 0, which)
+    codes[:] = 3
+    b.oracle_cache().put(int(b.table[0, at // 16]), at % 16, 0, which, codes, np.float16(bad), m)
+    cache, batch = b.device()
+    out = torch.empty_like(q)
+    cache.attention(batch, q, 1 / 8, out, u.workspace(cache, heads, 1, new, 400))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:new // 2], want[:new // 2])
+    if which == 1 or bad == "nan":
+        assert not out[new // 2:].isfinite().all(1).any()
+
+
+def test_hundreds_of_sequences(tern):
+    # more sequences than threads: the search for a CTA's share takes several turns
+    new = np.array([1, 0, 2, 1, 1] * 200)
+    length = new + np.arange(1000) % 7
+    b = util().Batch(new, length, 1, 64, 16, seed=27)
+    b.fill_values()
+    run_attention(tern, b, 2)
+    new = np.array([0, 1, 1, 1, 20] + [1] * 900)
+    b = util().Batch(new, new + 3, 1, 64, 16, seed=28)
+    b.fill_values()
+    run_attention(tern, b, 2)                             # one prompt among nine hundred single tokens
+
+
+def test_prompts_cut_between_ctas(tern):
+    # long histories and few rows: one tile's blocks go to several CTAs; the join's order is fixed
+    u = util()
+    b = u.Batch([10, 6], [6000, 3000], 1, 64, 64, seed=29)
+    b.fill_values()
+    q, first = run_attention(tern, b, 4)
+    cache, batch = b.device()
+    ws = u.workspace(cache, 4, 2, 10, 6000)
+    for _ in range(3):
+        out = torch.empty_like(q)
+        cache.attention(batch, q, 1 / 8, out, ws)
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("page_entry", [10 ** 6, -1])
+def test_bad_page_in_a_prompt(tern, page_entry):
+    u = util()
+    good = u.Batch([50, 40], [60, 90], 2, 64, 16, seed=30)
+    good.fill_values()
+    b = u.Batch([50, 40], [60, 90], 2, 64, 16, seed=30)
+    b.raw = good.raw.copy()
+    b.table[0, 2] = page_entry                            # positions 32 .. 47 of the first sequence
+    q = torch.randn((90, 128), device="cuda").bfloat16()
+    outs = []
+    for x in (b, good):
+        cache, batch = x.device()
+        o = torch.full_like(q, 9.0)
+        cache.attention(batch, q, 0.1, o, u.workspace(cache, 2, 2, 50, 90))
+        assert tern.device_error() == (tern.EFORMAT if x is b else tern.OK)
+        outs.append(o)
+    assert torch.equal(outs[0][50:], outs[1][50:])
+    ref, tol = attention_without(good, q, 0.1, 0, range(32, 48))
+    got = outs[0][:50].float().cpu().numpy().reshape(50, 2, 64)
+    # the expanded operands' own terms: scores off by 2^-11 sum |q| |k|, values and probabilities by 2^-11 each
+    qn = np.abs(q[:50].float().cpu().numpy().reshape(50, 2, 64)).sum(2, keepdims=True)
+    assert (np.abs(got - ref) <= tol + 2.0 ** -10 * 5 + 2 * 2.0 ** -11 * 0.1 * qn * 5 * 5).all()
+
+
 def test_bounds_larger_than_the_batch(tern):
     b = util().Batch([1, 2], [70, 40], 1, 64, 16, seed=17)
     b.fill_values()

@@ -227,3 +227,39 @@ def test_prompt_handed_to_the_decode_step(tern):
     decode.decode_layer(host(h0), lw, st.m.gains[0], ref_k[0], ref_v[0], n, decode.rope_cos_sin(n), first=1, last=2, rec=rec)
     got = host(trace[0])[H * HD + 2 * KVH * HD:]
     assert np.abs(got - rec["attn"]).max() <= 1e-4 * np.abs(rec["attn"]).max()
+
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from packed_ternary_weight_b200 import tern
+z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
+x, w, y = z(64, 512, dt=torch.int8) + 1, z(512, 512, dt=torch.int8) + 1, z(64, 512)
+sx, sw = z(64) + 1, z(512) + 1
+xf, xq, xs, gain = z(64, 512) + 1, z(64, 512, dt=torch.int8), z(64), z(512) + 1
+cache = tern.KV4Cache(z(8 * 2 * 16 * 72, dt=torch.uint8), 2, 64, 16)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+batch = tern.KV4Batch(i32([0, 64]), i32([64]), i32([[0, 1, 2, 3]]), 64, 64, 64)
+q, k, qo, rope = z(64, 128) + 1, z(64, 128) + 1, z(64, 128, dt=torch.bfloat16), z(64, 32, 2)
+rope[..., 0] = 1
+out, ws = torch.empty_like(qo), z(cache.attention_workspace_size(1, 64, 64, 2), dt=torch.uint8)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    tern.gemm_i8(x, sx, w, sw, y)
+    tern.norm_quantize(tern.NORM_PLAIN, xf, None, gain, 1e-5, None, xq, xs)
+    cache.append(batch, q, k, k, rope, qo)
+    cache.attention(batch, qo, 0.125, out, ws)
+g.replay()
+torch.cuda.synchronize()
+assert (y == 512).all() and (xq == 127).all() and (out == 1).all() and tern.device_error() == tern.OK
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
