@@ -3,11 +3,11 @@
 // with one fp16 (scale, min) pair: 4.25 bits per value at D = 128, against 16
 // of the decode step's bf16 cache.
 //
-// A group of D / 8 lanes takes one (token, head) at a time: lane l holds the
-// dimensions 4l .. 4l + 3 and D/2 + 4l .. + 3, the pairs that rotate_half combines,
-// so the rotation needs no exchange and each lane's codes are two pairs of whole
-// bytes. Minimum and maximum go over the group by shuffles. A warp takes one
-// head per group of a few tokens and up to six of each of many: the search for
+// A group of D / 16 lanes takes one (token, head) at a time: lane l holds the
+// dimensions 8l .. 8l + 7 and D/2 + 8l .. + 7, the pairs that rotate_half combines,
+// so the rotation needs no exchange, bf16 rows are read in 16-byte pieces and each
+// lane's codes are two whole words. Minimum and maximum go over the group by shuffles. A warp takes one
+// head per group of a few tokens and up to three of each of many: the search for
 // the token's sequence, its rotation row and its page are then shared by them,
 // and the heads' loads are issued together, ahead of that search.
 #include <cuda_bf16.h>
@@ -40,38 +40,53 @@ __device__ __forceinline__ int seq_of(const Kv4Params& c, int t) {
   return lo < c.seqs ? lo : -1;
 }
 
-// Four elements as they stand in memory.
+// Eight elements as they stand in memory.
 template <typename T>
-struct Raw4 {
-  uint4 u;
-  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void values(float (&v)[4]) const {
-    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+struct Raw8 {
+  uint4 u, w;
+  __device__ __forceinline__ void load(const T* p) {
+    u = reinterpret_cast<const uint4*>(p)[0];
+    w = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t e[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(e[i]);
   }
 };
 template <>
-struct Raw4<__nv_bfloat16> {
-  uint2 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void values(float (&v)[4]) const {
-    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(e[i] << 16);
+      v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+    }
   }
 };
-__device__ __forceinline__ void st4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float (&v)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    e[i] = *reinterpret_cast<const uint32_t*>(&a);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
 }
 
-constexpr int kMaxHeads = 6;  // of a token that a group of lanes takes
+constexpr int kMaxHeads = 3;  // of a token that a group of lanes takes
 
 // A warp's token and the heads of its groups: first, first + step, .. (count of them, the same in both groups).
 template <int D>
 struct Place {
-  static constexpr int L = D / 8, kGroups = 32 / L;
+  static constexpr int L = D / 16, kGroups = 32 / L;
   int t, first, step, gl;
   __device__ __forceinline__ bool find(const Kv4Params& c, int warps_per_token) {
     const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -92,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
   Place<D> pl;
   if (!pl.find(c, p.warps_per_token)) return;
   const int t = pl.t, gl = pl.gl;
-  Raw4<T> lo[HEADS], hi[HEADS];
+  Raw8<T> lo[HEADS], hi[HEADS];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int g = min(pl.first + i * pl.step, total - 1);
@@ -100,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
                    : g < c.heads + c.kv_heads
                        ? static_cast<const T*>(p.k) + (int64_t)t * p.ldk + (size_t)(g - c.heads) * D
                        : static_cast<const T*>(p.v) + (int64_t)t * p.ldv + (size_t)(g - c.heads - c.kv_heads) * D;
-    lo[i].load(src + 4 * gl);
-    hi[i].load(src + D / 2 + 4 * gl);
+    lo[i].load(src + 8 * gl);
+    hi[i].load(src + D / 2 + 8 * gl);
   }
   const int s = seq_of(c, t);
   if (s < 0) return;
@@ -114,43 +129,48 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
   const bool skip = pos < 0 || pos >= p.max_pos;  // not stored, its query is zero
   if (pos >= p.max_pos) kv4::report_bad();
   int page = -1;
-  float4 cs0 = make_float4(0.f, 0.f, 0.f, 0.f), cs1 = cs0;
+  float co[8], si[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) co[k] = si[k] = 0.f;
   if (!skip) {
     page = kv4::page_of(c, s, pos);
     if (page < 0) kv4::report_bad();
-    const float4* row = reinterpret_cast<const float4*>(p.rope + ((size_t)pos * (D / 2) + 4 * gl) * 2);
-    cs0 = __ldg(row);
-    cs1 = __ldg(row + 1);
+    const float4* row = reinterpret_cast<const float4*>(p.rope + ((size_t)pos * (D / 2) + 8 * gl) * 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 cs = __ldg(row + k);
+      co[2 * k] = cs.x, si[2 * k] = cs.y, co[2 * k + 1] = cs.z, si[2 * k + 1] = cs.w;
+    }
   }
-  const float co[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, si[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int g = pl.first + i * pl.step;
     const bool is_q = g < c.heads, is_k = !is_q && g < c.heads + c.kv_heads;
-    float a[4], b[4];
+    float a[8], b[8];
     lo[i].values(a);
     hi[i].values(b);
     if (is_q || is_k) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const float x = a[k], y = b[k];
         a[k] = __fsub_rn(__fmul_rn(x, co[k]), __fmul_rn(y, si[k]));
         b[k] = __fadd_rn(__fmul_rn(y, co[k]), __fmul_rn(x, si[k]));
       }
     }
     if (is_q) {
-      __nv_bfloat16* qo = reinterpret_cast<__nv_bfloat16*>(p.q_out) + ((size_t)t * c.heads + g) * D + 4 * gl;
+      __nv_bfloat16* qo = reinterpret_cast<__nv_bfloat16*>(p.q_out) + ((size_t)t * c.heads + g) * D + 8 * gl;
       if (skip) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = b[k] = 0.f;
+        for (int k = 0; k < 8; ++k) a[k] = b[k] = 0.f;
       }
-      st4(qo, a);
-      st4(qo + D / 2, b);
+      st8(qo, a);
+      st8(qo + D / 2, b);
     }
     // a warp whose groups all hold queries skips the rest
     if (__all_sync(0xffffffffu, is_q || g >= total)) continue;
-    float mn = fminf(fminf(fminf(a[0], a[1]), fminf(a[2], a[3])), fminf(fminf(b[0], b[1]), fminf(b[2], b[3])));
-    float mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
+    float mn = a[0], mx = a[0];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mn = fminf(mn, fminf(a[k], b[k])), mx = fmaxf(mx, fmaxf(a[k], b[k]));
 #pragma unroll
     for (int o = Place<D>::L / 2; o; o >>= 1) {
       mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -164,14 +184,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
     auto code = [&](float v) {
       return (unsigned)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(v, m), inv))));
     };
-    auto four = [&](const float (&v)[4]) {
-      return (uint16_t)(code(v[0]) | (code(v[1]) << 4) | (code(v[2]) << 8) | (code(v[3]) << 12));
+    auto eight = [&](const float (&v)[8]) {
+      unsigned w = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w |= code(v[k]) << (4 * k);
+      return w;
     };
     uint8_t* blk = c.pages + kv4::block_offset(c, page, head);
     const int slot = pos & (c.page - 1);
-    uint16_t* row = reinterpret_cast<uint16_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
-    row[gl] = four(a);
-    row[D / 8 + gl] = four(b);
+    uint32_t* row = reinterpret_cast<uint32_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
+    row[gl] = eight(a);
+    row[D / 16 + gl] = eight(b);
     if (gl == 0)
       *reinterpret_cast<__half2*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4)) =
           __halves2half2(hs, hm);
@@ -204,10 +227,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
     u[i] = v[i] = pair[i] = 0u;
     if (page >= 0) {
       const uint8_t* blk = c.pages + kv4::block_offset(c, page, is_k ? g : g - c.kv_heads);
-      const uint16_t* row =
-          reinterpret_cast<const uint16_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
+      const uint32_t* row =
+          reinterpret_cast<const uint32_t*>(blk + (size_t)(is_k ? 0 : c.page * (D / 2)) + (size_t)slot * (D / 2));
       u[i] = row[gl];
-      v[i] = row[D / 8 + gl];
+      v[i] = row[D / 16 + gl];
       pair[i] = *reinterpret_cast<const uint32_t*>(blk + (size_t)c.page * D + (size_t)slot * 8 + (is_k ? 0 : 4));
     }
   }
@@ -219,16 +242,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
     void* dst = is_k ? p.k : p.v;
     if (!dst) continue;
     const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pair[i]));
-    T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)(is_k ? g : g - c.kv_heads) * D + 4 * gl;
+    T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)(is_k ? g : g - c.kv_heads) * D + 8 * gl;
     // scale * code is exact in fp32 (11 + 4 bits), so the fused form rounds once, as the definition
-    float a[4], b[4];
+    float a[8], b[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       a[k] = page < 0 ? 0.f : __fmaf_rn(sm.x, (float)((u[i] >> (4 * k)) & 15u), sm.y);
       b[k] = page < 0 ? 0.f : __fmaf_rn(sm.x, (float)((v[i] >> (4 * k)) & 15u), sm.y);
     }
-    st4(out, a);
-    st4(out + D / 2, b);
+    st8(out, a);
+    st8(out + D / 2, b);
   }
 }
 
@@ -241,11 +264,11 @@ struct Spread {
   long long blocks;
 };
 Spread spread(const Kv4Params& c, int total) {
-  const int groups = 32 / (c.dim / 8);
+  const int groups = 32 / (c.dim / 16);
   const long long warps = (long long)c.tokens * ((total + groups - 1) / groups);  // with one head each
   const long long many = warps / (24ll * sm_count());
   Spread s;
-  s.heads = many >= kMaxHeads ? kMaxHeads : (many >= 3 ? 3 : 1);
+  s.heads = many >= kMaxHeads ? kMaxHeads : 1;
   s.warps_per_token = (total + s.heads * groups - 1) / (s.heads * groups);
   s.blocks = ((long long)c.tokens * s.warps_per_token + kThreads / 32 - 1) / (kThreads / 32);
   return s;
@@ -255,14 +278,12 @@ template <int D, typename T>
 void append_any(const Kv4AppendParams& p, const Spread& sp, cudaStream_t s) {
   const unsigned grid = (unsigned)sp.blocks;
   if (sp.heads == kMaxHeads) append_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
-  else if (sp.heads == 3) append_kernel<D, T, 3><<<grid, kThreads, 0, s>>>(p);
   else append_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
 }
 template <int D, typename T>
 void read_any(const Kv4ReadParams& p, const Spread& sp, cudaStream_t s) {
   const unsigned grid = (unsigned)sp.blocks;
   if (sp.heads == kMaxHeads) read_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
-  else if (sp.heads == 3) read_kernel<D, T, 3><<<grid, kThreads, 0, s>>>(p);
   else read_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
 }
 
