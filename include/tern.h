@@ -400,8 +400,8 @@ typedef enum { TERN_NORM_PLAIN = 1, TERN_NORM_ADD = 2, TERN_NORM_RELU2 = 3 } ter
  *     update in place, with the same stride);
  *   d_xq int8 [m][k], ldq >= k (tern_gemm_batched wants ldq = k, tern_gemm_i8 a
  *     multiple of 16); d_xscale float [m].
- * Any k and any stride; rows of k <= 16384 with k and the strides multiples of 4
- * and 16-byte aligned pointers are read once. TERN_EALIGN: a pointer not aligned
+ * Any k and any stride; rows of k <= 16384, k a multiple of 8, that start on 16-byte
+ * (d_xq: 8-byte) boundaries are read once. TERN_EALIGN: a pointer not aligned
  * to its element.
  */
 tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, tern_out x_type, const void* d_x, int64_t ldx,

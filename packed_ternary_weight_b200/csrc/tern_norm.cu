@@ -101,33 +101,79 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
   if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : 0.f;
 }
 
-// Four elements as they stand in memory, and their values.
+// Two fp32 operations in one instruction, each rounded as its own (only where no
+// product meets a sum: the compiler makes one rounding of such a packed pair).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Eight elements as they stand in memory, and their values.
 template <typename T>
-struct Raw4 {
-  uint4 u;
-  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ float4 value() const {
-    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+struct Raw8 {
+  uint4 u, w;
+  __device__ __forceinline__ void load(const T* p) {
+    u = reinterpret_cast<const uint4*>(p)[0];
+    w = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { u = w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float2 (&v)[4]) const {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+    v[2] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[3] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
 };
 template <>
-struct Raw4<__nv_bfloat16> {
-  uint2 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
-  __device__ __forceinline__ float4 value() const {
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float2 (&v)[4]) const {
+    const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(e[i] << 16), __uint_as_float(e[i] & 0xFFFF0000u));
   }
 };
-__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void st8(float* p, const float2 (&v)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void st8(__nv_bfloat16* p, const float2 (&v)[4]) {
+  uint32_t e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[i].x, v[i].y);
+    e[i] = *reinterpret_cast<const uint32_t*>(&a);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
+}
+template <int MODE, typename RT>
+__device__ __forceinline__ float2 combine2(float2 x, float2 r) {
+  if constexpr (MODE == TERN_NORM_ADD) {
+    const float2 v = add2(x, r);
+    return make_float2(round_to(v.x, static_cast<const RT*>(nullptr)), round_to(v.y, static_cast<const RT*>(nullptr)));
+  }
+  if constexpr (MODE == TERN_NORM_RELU2) {
+    const float2 g = make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f));
+    return mul2(mul2(g, g), r);
+  }
+  return x;
 }
 
-// Rows read once: thread i holds the vectors of four i, i + T, .. (NV of them) in
+// Rows read once: thread i holds the vectors of eight i, i + T, .. (NV of them) in
 // registers through all three steps, and the next row's are on their way meanwhile
 // (a block takes the rows blockIdx, blockIdx + grid, ..): the kernel is bound by
 // memory once the three block-wide steps of a row are hidden behind the next row's loads.
@@ -135,110 +181,118 @@ template <int MODE, typename XT, typename RT, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p) {
   __shared__ double red[33];
   __shared__ float redf[2][32];
-  const int k = p.k, T = blockDim.x;
-  Raw4<XT> xw[NV];
-  Raw4<RT> rw[NV];
+  const int k = p.k, T = blockDim.x, first = 8 * (int)threadIdx.x, step = 8 * T;
+  Raw8<XT> xw[NV];
+  Raw8<RT> rw[NV];
   auto load = [&](int row) {
+    const XT* x = static_cast<const XT*>(p.x) + (int64_t)row * p.ldx + first;
+    const RT* r = static_cast<const RT*>(p.r) + (int64_t)row * p.ldr + first;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = 4 * (j * T + (int)threadIdx.x);
       xw[j].zero();
       rw[j].zero();
-      if (row < p.m && i < k) {
-        xw[j].load(static_cast<const XT*>(p.x) + (int64_t)row * p.ldx + i);
-        if (MODE != TERN_NORM_PLAIN) rw[j].load(static_cast<const RT*>(p.r) + (int64_t)row * p.ldr + i);
+      if (row < p.m && first + j * step < k) {
+        xw[j].load(x + j * step);
+        if (MODE != TERN_NORM_PLAIN) rw[j].load(r + j * step);
       }
     }
   };
   load(blockIdx.x);
   int turn = 0;
   for (int row = blockIdx.x; row < p.m; row += gridDim.x, turn ^= 1) {
-  float4 v[NV];
-  double s0 = 0.0, s1 = 0.0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = 4 * (j * T + (int)threadIdx.x);
-    const float4 x = xw[j].value(), r = rw[j].value();
-    v[j] = make_float4(combine<MODE, RT>(x.x, r.x), combine<MODE, RT>(x.y, r.y), combine<MODE, RT>(x.z, r.z),
-                       combine<MODE, RT>(x.w, r.w));
-    if (MODE == TERN_NORM_ADD && i < k) st4(static_cast<RT*>(p.sum) + (int64_t)row * p.ldsum + i, v[j]);
-    s0 = fma((double)v[j].x, (double)v[j].x, s0);
-    s1 = fma((double)v[j].y, (double)v[j].y, s1);
-    s0 = fma((double)v[j].z, (double)v[j].z, s0);
-    s1 = fma((double)v[j].w, (double)v[j].w, s1);
-  }
-  load(row + gridDim.x);
-  const float f = row_factor(s0 + s1, k, p.eps, red);
-  float a = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = 4 * (j * T + (int)threadIdx.x);
-    if (i < k) {
-      const float4 g = __ldg(reinterpret_cast<const float4*>(p.gain + i));
-      v[j] = make_float4(__fmul_rn(__fmul_rn(v[j].x, f), g.x), __fmul_rn(__fmul_rn(v[j].y, f), g.y),
-                         __fmul_rn(__fmul_rn(v[j].z, f), g.z), __fmul_rn(__fmul_rn(v[j].w, f), g.w));
-      a = fmaxf(a, fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w))));
-    }
-  }
-  a = row_max(a, redf[turn]);
-  const float inv = a > 0.f ? __fdiv_rn(127.0f, a) : 0.f;
-  // |y| <= a, so |y inv| is at most 127 (1 + 2^-22): the sum with 1.5 * 2^23 rounds it to the integer (ties to even)
-  // that its low byte holds, and no clamp is needed; an infinite inv (a tiny row) takes the definition's steps
-  auto low = [&](float y) { return __float_as_uint(__fadd_rn(__fmul_rn(y, inv), 12582912.f)); };
-  auto q = [&](float y) { return (uint32_t)(y != 0.f ? quant(y, inv) : 0) & 0xFFu; };
-  int8_t* out = p.xq + (int64_t)row * p.ldq;
-  auto store = [&](auto word) {
+    float2 v[NV][4];
+    double s0 = 0.0, s1 = 0.0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int i = 4 * (j * T + (int)threadIdx.x);
-      if (i < k) *reinterpret_cast<uint32_t*>(out + i) = word(v[j]);
+      float2 r[4];
+      xw[j].values(v[j]);
+      rw[j].values(r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[j][e] = combine2<MODE, RT>(v[j][e], r[e]);
+        s0 = fma((double)v[j][e].x, (double)v[j][e].x, s0);
+        s1 = fma((double)v[j][e].y, (double)v[j][e].y, s1);
+      }
+      if (MODE == TERN_NORM_ADD && first + j * step < k)
+        st8(static_cast<RT*>(p.sum) + (int64_t)row * p.ldsum + first + j * step, v[j]);
     }
-  };
-  if (inv != INFINITY)
-    store([&](float4 y) {
-      return __byte_perm(__byte_perm(low(y.x), low(y.y), 0x0040), __byte_perm(low(y.z), low(y.w), 0x0040), 0x5410);
-    });
-  else
-    store([&](float4 y) { return q(y.x) | (q(y.y) << 8) | (q(y.z) << 16) | (q(y.w) << 24); });
-  if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : 0.f;
+    load(row + gridDim.x);
+    const float f = row_factor(s0 + s1, k, p.eps, red);
+    const float2 f2 = make_float2(f, f);
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (first + j * step < k) {
+        const float4* g = reinterpret_cast<const float4*>(p.gain + first + j * step);
+        const float4 g0 = __ldg(g), g1 = __ldg(g + 1);
+        const float2 gain[4] = {make_float2(g0.x, g0.y), make_float2(g0.z, g0.w), make_float2(g1.x, g1.y),
+                                make_float2(g1.z, g1.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[j][e] = mul2(mul2(v[j][e], f2), gain[e]);
+          a = fmaxf(a, fmaxf(fabsf(v[j][e].x), fabsf(v[j][e].y)));
+        }
+      }
+    }
+    a = row_max(a, redf[turn]);
+    const float inv = a > 0.f ? __fdiv_rn(127.0f, a) : 0.f;
+    int8_t* out = p.xq + (int64_t)row * p.ldq + first;
+    auto store = [&](auto word) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (first + j * step < k)
+          *reinterpret_cast<uint2*>(out + j * step) = make_uint2(word(v[j][0], v[j][1]), word(v[j][2], v[j][3]));
+    };
+    if (inv != INFINITY) {
+      // |y| <= a, so |y inv| is at most 127 (1 + 2^-22): the sum with 1.5 * 2^23 rounds it to the integer (ties to
+      // even) that its low byte holds, and no clamp is needed
+      // (one by one: the packed product and sum are contracted into one rounding)
+      auto low = [&](float y) { return __float_as_uint(__fadd_rn(__fmul_rn(y, inv), 12582912.f)); };
+      store([&](float2 x, float2 y) {
+        return __byte_perm(__byte_perm(low(x.x), low(x.y), 0x0040), __byte_perm(low(y.x), low(y.y), 0x0040), 0x5410);
+      });
+    } else {  // a tiny row takes the definition's steps
+      auto q = [&](float y) { return (uint32_t)(y != 0.f ? quant(y, inv) : 0) & 0xFFu; };
+      store([&](float2 x, float2 y) { return q(x.x) | (q(x.y) << 8) | (q(y.x) << 16) | (q(y.y) << 24); });
+    }
+    if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : 0.f;
   }
 }
 
-// Whether a row can be read in vectors of four.
+// Whether a row can be read in vectors of eight.
 bool vectors(const NormParams& p) {
-  auto ok = [](const void* q, int64_t ld, int bytes) {
-    return !q || ((reinterpret_cast<uintptr_t>(q) & (uintptr_t)(4 * bytes - 1)) == 0 && (ld & 3) == 0);
+  auto ok = [](const void* q, int64_t ld, int bytes) {  // 16-byte pieces; 8 bytes of codes
+    const int unit = bytes == 1 ? 8 : 16;
+    return !q || ((reinterpret_cast<uintptr_t>(q) & (uintptr_t)(unit - 1)) == 0 && ld * bytes % unit == 0);
   };
-  return p.k % 4 == 0 && ok(p.x, p.ldx, p.x_bf16 ? 2 : 4) && ok(p.r, p.ldr, p.r_bf16 ? 2 : 4) &&
+  return p.k % 8 == 0 && ok(p.x, p.ldx, p.x_bf16 ? 2 : 4) && ok(p.r, p.ldr, p.r_bf16 ? 2 : 4) &&
          ok(p.sum, p.ldsum, p.r_bf16 ? 2 : 4) && ok(p.xq, p.ldq, 1) && ok(p.gain, 4, 4);
 }
 
-// Vectors per thread: four where there are rows enough to fill the device, one
+// Vectors per thread: two where there are rows enough to fill the device, one
 // where a row's latency counts (1 x 2560: 2.7 us, 6.6 us with the row read three
-// times by 256 threads); more only where a block of 1024 threads needs them. Then
-// 640 threads per multiprocessor, at least two blocks, with registers for the
-// next row: 8192 x 4096 with the residual 64 us (0.89 of the measured copy rate;
-// 69 us with 1024 threads), 4096 x 2560 26 us (32 us with two blocks); 2043 x 6912
-// gated 22 us (0.5 of the copy rate: bound by instruction issue; 27 us with one block).
+// times by 256 threads) and a block's threads suffice. About 1024 threads per
+// multiprocessor, the registers of the next row included: 8192 x 4096 with the
+// residual 62 us (0.92 of the measured copy rate; 76 us with 640 threads), 4096 x
+// 2560 27 us, 2043 x 6912 gated 19 us (0.57 of the copy rate: bound by instruction
+// issue).
 template <int MODE, typename XT, typename RT>
 int launch_mode(const NormParams& p, cudaStream_t s) {
-  const int nv = p.k / 4;
-  if (nv > 4096 || !vectors(p)) {
+  const int nv = p.k / 8;
+  if (nv > 2048 || !vectors(p)) {
     norm_any_kernel<MODE, XT, RT><<<p.m, 256, 0, s>>>(p);
     return (int)cudaGetLastError();
   }
   const bool few = p.m < 2 * sm_count();
-  const int per = nv > 2048 ? 4 : (few ? (nv > 1024 ? 2 : 1) : 4);
+  const int per = nv > 1024 || !few ? 2 : 1;
   const int threads = std::max(64, ((nv + per - 1) / per + 31) / 32 * 32);
-  const int grid = std::min(p.m, std::max(2, 640 / threads) * sm_count());
+  const int grid = std::min(p.m, std::max(2, 1024 / threads) * sm_count());
   if (per == 1)
     norm_row_kernel<MODE, XT, RT, 1, 1024, 1><<<grid, threads, 0, s>>>(p);
-  else if (per == 2)
-    norm_row_kernel<MODE, XT, RT, 2, 1024, 1><<<grid, threads, 0, s>>>(p);
   else if (threads <= 512)
-    norm_row_kernel<MODE, XT, RT, 4, 512, 2><<<grid, threads, 0, s>>>(p);
+    norm_row_kernel<MODE, XT, RT, 2, 512, 2><<<grid, threads, 0, s>>>(p);
   else
-    norm_row_kernel<MODE, XT, RT, 4, 1024, 1><<<grid, threads, 0, s>>>(p);
+    norm_row_kernel<MODE, XT, RT, 2, 1024, 1><<<grid, threads, 0, s>>>(p);
   return (int)cudaGetLastError();
 }
 

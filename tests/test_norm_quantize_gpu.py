@@ -68,6 +68,14 @@ def test_row_counts(tern, m):
     check(tern, "add", m, 512, "bf16", "f32", seed=m)
 
 
+@pytest.mark.parametrize("seed", range(6))
+def test_borders_of_the_rounding(tern, seed):
+    # enough values that some stand at a half after the product's own rounding, where a fused product and sum would
+    # round the other way (one in about 2^17 values)
+    check(tern, "plain", 300, 4096, "bf16", "f32", seed=seed)
+    check(tern, "relu2", 40, 6912, "f32", "f32", seed=seed)
+
+
 @pytest.mark.parametrize("pad", [1, 4, 8])
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
 def test_strides(tern, pad, xt):
