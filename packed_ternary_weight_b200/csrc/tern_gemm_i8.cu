@@ -33,6 +33,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "tern_launch.cuh"
 #include "tern_tc.cuh"
 
 namespace tern {
@@ -128,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc::fence_before_sync();
+  pdl_launch_dependents();
+  pdl_wait();
   __syncthreads();
   if constexpr (PAIR) {  // both CTAs' barriers exist before either signals the other's
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -414,20 +417,7 @@ int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream) {
   const int bytes = kSmemTop, cluster = a.pl.pair ? 2 : a.pl.split;
   const int rc = allow_smem(reinterpret_cast<const void*>(kernel), bytes);
   if (rc != 0) return rc;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.pl.grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)bytes;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  if (cluster > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, mw, mx);
-  return e != cudaSuccess ? (int)e : (int)cudaGetLastError();
+  return launch_dependent(kernel, a.pl.grid, kThreads, (size_t)bytes, cluster, static_cast<cudaStream_t>(stream), a, mw, mx);
 }
 
 }  // namespace tern

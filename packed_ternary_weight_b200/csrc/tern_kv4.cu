@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "tern_kv4.cuh"
+#include "tern_launch.cuh"
 
 namespace tern {
 
@@ -102,6 +103,8 @@ struct Place {
 
 template <int D, typename T, int HEADS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const Kv4Params& c = p.c;
   const int total = c.heads + 2 * c.kv_heads;  // of a token: q heads, k heads, v heads
   Place<D> pl;
@@ -203,6 +206,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
 
 template <int D, typename T, int HEADS>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const Kv4Params& c = p.c;
   const int total = 2 * c.kv_heads;
   Place<D> pl;
@@ -275,16 +280,14 @@ Spread spread(const Kv4Params& c, int total) {
 }
 
 template <int D, typename T>
-void append_any(const Kv4AppendParams& p, const Spread& sp, cudaStream_t s) {
-  const unsigned grid = (unsigned)sp.blocks;
-  if (sp.heads == kMaxHeads) append_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
-  else append_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
+int append_any(const Kv4AppendParams& p, const Spread& sp, cudaStream_t s) {
+  return launch_dependent(sp.heads == kMaxHeads ? append_kernel<D, T, kMaxHeads> : append_kernel<D, T, 1>,
+                          (int)sp.blocks, kThreads, 0, 1, s, p);
 }
 template <int D, typename T>
-void read_any(const Kv4ReadParams& p, const Spread& sp, cudaStream_t s) {
-  const unsigned grid = (unsigned)sp.blocks;
-  if (sp.heads == kMaxHeads) read_kernel<D, T, kMaxHeads><<<grid, kThreads, 0, s>>>(p);
-  else read_kernel<D, T, 1><<<grid, kThreads, 0, s>>>(p);
+int read_any(const Kv4ReadParams& p, const Spread& sp, cudaStream_t s) {
+  return launch_dependent(sp.heads == kMaxHeads ? read_kernel<D, T, kMaxHeads> : read_kernel<D, T, 1>,
+                          (int)sp.blocks, kThreads, 0, 1, s, p);
 }
 
 }  // namespace
@@ -293,18 +296,16 @@ int launch_kv4_append(Kv4AppendParams p, void* stream) {
   const Spread sp = spread(p.c, p.c.heads + 2 * p.c.kv_heads);
   p.warps_per_token = sp.warps_per_token;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.c.dim == 128) p.bf16 ? append_any<128, __nv_bfloat16>(p, sp, s) : append_any<128, float>(p, sp, s);
-  else p.bf16 ? append_any<64, __nv_bfloat16>(p, sp, s) : append_any<64, float>(p, sp, s);
-  return (int)cudaGetLastError();
+  if (p.c.dim == 128) return p.bf16 ? append_any<128, __nv_bfloat16>(p, sp, s) : append_any<128, float>(p, sp, s);
+  return p.bf16 ? append_any<64, __nv_bfloat16>(p, sp, s) : append_any<64, float>(p, sp, s);
 }
 
 int launch_kv4_read(Kv4ReadParams p, void* stream) {
   const Spread sp = spread(p.c, 2 * p.c.kv_heads);
   p.warps_per_token = sp.warps_per_token;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.c.dim == 128) p.bf16 ? read_any<128, __nv_bfloat16>(p, sp, s) : read_any<128, float>(p, sp, s);
-  else p.bf16 ? read_any<64, __nv_bfloat16>(p, sp, s) : read_any<64, float>(p, sp, s);
-  return (int)cudaGetLastError();
+  if (p.c.dim == 128) return p.bf16 ? read_any<128, __nv_bfloat16>(p, sp, s) : read_any<128, float>(p, sp, s);
+  return p.bf16 ? read_any<64, __nv_bfloat16>(p, sp, s) : read_any<64, float>(p, sp, s);
 }
 
 tern_status kv4_check(const tern_kv4_cache* cache, const tern_kv4_batch* batch, Kv4Params* c) {

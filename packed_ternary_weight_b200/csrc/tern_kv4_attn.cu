@@ -58,6 +58,7 @@
 #include <cmath>
 
 #include "tern_kv4.cuh"
+#include "tern_launch.cuh"
 #include "tern_tc.cuh"
 
 namespace tern {
@@ -314,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
     sm.abort = 0;
     fence_mbar_init();
   }
+  pdl_launch_dependents();
+  pdl_wait();
   __syncthreads();
   volatile uint32_t* abort = &sm.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -605,8 +608,7 @@ int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
   constexpr int bytes = (int)sizeof(Shared<D, NT>);
   const int rc = allow_smem(reinterpret_cast<const void*>(attn_kernel<D, NT>), bytes);
   if (rc != 0) return rc;
-  attn_kernel<D, NT><<<ctas, kThreads, bytes, s>>>(p);
-  return (int)cudaGetLastError();
+  return launch_dependent(attn_kernel<D, NT>, ctas, kThreads, bytes, 1, s, p);
 }
 
 // How a batch within these bounds runs. Sequences of up to 16 query rows per kv

@@ -41,6 +41,7 @@
 #include <algorithm>
 
 #include "tern_kv4.cuh"
+#include "tern_launch.cuh"
 #include "tern_tc.cuh"
 
 namespace tern {
@@ -229,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   const Kv4Params& c = p.c;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   volatile uint32_t* misc = ctl.misc;
+  pdl_launch_dependents();
+  pdl_wait();
 
   kv4::Share sh;
   auto weight = [&](int i, bool report) -> long long {
@@ -703,8 +706,7 @@ int launch_dim(const Kv4PromptParams& p, int ctas, cudaStream_t s) {
   constexpr int bytes = 1024 + kCtlBytes + 6 * (D / 64) * kSub;
   const int rc = allow_smem(reinterpret_cast<const void*>(prompt_kernel<D>), bytes);
   if (rc != 0) return rc;
-  prompt_kernel<D><<<ctas, kThreads, bytes, s>>>(p);
-  return (int)cudaGetLastError();
+  return launch_dependent(prompt_kernel<D>, ctas, kThreads, bytes, 1, s, p);
 }
 
 }  // namespace

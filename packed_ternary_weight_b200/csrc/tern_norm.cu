@@ -11,6 +11,8 @@
 #include <algorithm>
 
 #include "tern_internal.h"
+#include "tern_launch.cuh"
+#include "tern_ptx.cuh"
 
 namespace tern {
 namespace {
@@ -73,6 +75,8 @@ template <int MODE, typename XT, typename RT>
 __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
   __shared__ double red[33];
   __shared__ float redf[32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int row = blockIdx.x, k = p.k;
   const XT* x = static_cast<const XT*>(p.x) + (int64_t)row * p.ldx;
   const RT* r = MODE == TERN_NORM_PLAIN ? nullptr : static_cast<const RT*>(p.r) + (int64_t)row * p.ldr;
@@ -181,6 +185,8 @@ template <int MODE, typename XT, typename RT, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p) {
   __shared__ double red[33];
   __shared__ float redf[2][32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int k = p.k, T = blockDim.x, first = 8 * (int)threadIdx.x, step = 8 * T;
   Raw8<XT> xw[NV];
   Raw8<RT> rw[NV];
@@ -279,21 +285,14 @@ bool vectors(const NormParams& p) {
 template <int MODE, typename XT, typename RT>
 int launch_mode(const NormParams& p, cudaStream_t s) {
   const int nv = p.k / 8;
-  if (nv > 2048 || !vectors(p)) {
-    norm_any_kernel<MODE, XT, RT><<<p.m, 256, 0, s>>>(p);
-    return (int)cudaGetLastError();
-  }
+  if (nv > 2048 || !vectors(p)) return launch_dependent(norm_any_kernel<MODE, XT, RT>, p.m, 256, 0, 1, s, p);
   const bool few = p.m < 2 * sm_count();
   const int per = nv > 1024 || !few ? 2 : 1;
   const int threads = std::max(64, ((nv + per - 1) / per + 31) / 32 * 32);
   const int grid = std::min(p.m, std::max(2, 1024 / threads) * sm_count());
-  if (per == 1)
-    norm_row_kernel<MODE, XT, RT, 1, 1024, 1><<<grid, threads, 0, s>>>(p);
-  else if (threads <= 512)
-    norm_row_kernel<MODE, XT, RT, 2, 512, 2><<<grid, threads, 0, s>>>(p);
-  else
-    norm_row_kernel<MODE, XT, RT, 2, 1024, 1><<<grid, threads, 0, s>>>(p);
-  return (int)cudaGetLastError();
+  if (per == 1) return launch_dependent(norm_row_kernel<MODE, XT, RT, 1, 1024, 1>, grid, threads, 0, 1, s, p);
+  if (threads <= 512) return launch_dependent(norm_row_kernel<MODE, XT, RT, 2, 512, 2>, grid, threads, 0, 1, s, p);
+  return launch_dependent(norm_row_kernel<MODE, XT, RT, 2, 1024, 1>, grid, threads, 0, 1, s, p);
 }
 
 template <int MODE>
