@@ -400,7 +400,7 @@ typedef enum { TERN_NORM_PLAIN = 1, TERN_NORM_ADD = 2, TERN_NORM_RELU2 = 3 } ter
  *     update in place, with the same stride);
  *   d_xq int8 [m][k], ldq >= k (tern_gemm_batched wants ldq = k, tern_gemm_i8 a
  *     multiple of 16); d_xscale float [m].
- * Any k and any stride; rows of k <= 16384, k a multiple of 8, that start on 16-byte
+ * m, k <= 2^30. Any k and any stride; rows of k <= 16384, k a multiple of 8, that start on 16-byte
  * (d_xq: 8-byte) boundaries are read once. TERN_EALIGN: a pointer not aligned
  * to its element.
  */
@@ -419,7 +419,8 @@ tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, tern_out x_
  * token and head has its own scales, for keys (after RoPE) and for values x:
  *   min = fp16_rn(min x), scale = fp16_rn(fl(fl(max x - min x) / 15)),
  *   code = clamp(rint(fl(fl(x - min) fl(1 / scale))), 0, 15); scale 0: code 0.
- * Values must be finite and within the fp16 range (+-65504).
+ * Values must be finite and within +-65000: what the codes stand for, min + 15 scale
+ * at most, then stays in the fp16 range.
  */
 typedef struct tern_kv4_cache {
   int32_t kv_heads;   /* 1..1024 */
@@ -494,10 +495,11 @@ tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32
  * Causal attention of the batch's new tokens over the cache (which holds them
  * already): out = softmax(scale q k^T) v over the positions up to the token's
  * own. Query head h reads kv head h / (heads / kv_heads); heads is a multiple of
- * kv_heads, any ratio. Products on fp16 operands with fp32 accumulation: codes
- * are exact, q keeps every element within 2^38 of its row's largest,
- * probabilities times value scales are rounded to fp16; the softmax in fp32.
- * Scores must be finite in fp32.
+ * kv_heads, any ratio. Products on fp16 operands with fp32 accumulation, the softmax
+ * in fp32; q keeps all bits of every element within 2^27 of its row's largest. Sequences with up
+ * to 16 new tokens x heads per kv head multiply by the codes, which are exact, and round
+ * probabilities times value scales to fp16; longer ones round keys, values and
+ * probabilities to fp16. Scores must be finite in fp32.
  *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.
  */
 tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, float scale,
@@ -511,6 +513,7 @@ tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch
  * tern_quantize_act on a weight matrix [n][k] gives d_w and d_wscale.
  *   d_x int8 [m][k], d_w int8 [n][k]: 16-byte aligned, row strides ldx, ldw >= k
  *   and multiples of 16 (bytes from k on are not used); k <= 131071;
+ *   m, n and the tiles of 16 tokens by 128 channels each at most 2^30;
  *   d_y [m][n], row stride ldy >= n. m = 0 does nothing.
  */
 tern_status tern_gemm_i8(int32_t m, int32_t n, int32_t k, const int8_t* d_x, int64_t ldx, const float* d_xscale,

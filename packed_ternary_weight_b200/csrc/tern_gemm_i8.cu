@@ -359,7 +359,7 @@ Plan make_plan(int m, int n, int k, int sms) {
   pl.tiles_n = (n + rows - 1) / rows;
   pl.steps = (k + kStepK - 1) / kStepK;
   const long long tiles = (long long)pl.tiles_n * pl.tiles_m;
-  pl.tiles = (int)std::min(tiles, 0x7FFFFFFFll);
+  pl.tiles = (int)tiles;
   pl.split = 1;
   if (!pl.pair && tiles <= sms / 2) {
     const int* fit = resident_clusters(sms);
@@ -426,10 +426,10 @@ extern "C" tern_status tern_gemm_i8(int32_t m, int32_t n, int32_t k, const int8_
                                     const float* d_xscale, const int8_t* d_w, int64_t ldw, const float* d_wscale,
                                     tern_out out, void* d_y, int64_t ldy, void* stream) {
   using namespace tern;
-  if (m < 0 || n < 1 || k < 1 || k > 131071 || ldx < k || ldw < k || ldy < n || ((ldx | ldw) & 15) != 0)
+  if (m < 0 || m > kMaxExtent || n < 1 || n > kMaxExtent || k < 1 || k > 131071 || ldx < k || ldw < k || ldy < n || ((ldx | ldw) & 15) != 0)
     return TERN_EINVAL;
   if (out != TERN_OUT_F32 && out != TERN_OUT_BF16) return TERN_EINVAL;
-  if ((int64_t)((m + 15) / 16) * ((n + 127) / 128) > 0x7FFFFFFFll) return TERN_EINVAL;
+  if ((int64_t)((m + 15) / 16) * ((n + 127) / 128) > kMaxExtent) return TERN_EINVAL;
   if (m == 0) return TERN_OK;
   if (!d_x || !d_xscale || !d_w || !d_wscale || !d_y) return TERN_EINVAL;
   if (((reinterpret_cast<uintptr_t>(d_x) | reinterpret_cast<uintptr_t>(d_w)) & 15u) != 0) return TERN_EALIGN;

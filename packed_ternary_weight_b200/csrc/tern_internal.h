@@ -395,6 +395,7 @@ struct GemmI8Params {
 int launch_gemm_i8(const GemmI8Params& p, int sms, void* stream);
 int read_clear_dev_error_gemm_i8(void* stream, unsigned* out);
 
+constexpr int kMaxExtent = 1 << 30;  // rows, columns and tiles, so that their sums with a grid's stay in 32 bits
 int sm_count();  // multiprocessors of the current device
 // cudaFuncSetAttribute of the dynamic shared memory, once per kernel and device; a cudaError_t
 int allow_smem(const void* kernel, int bytes);

@@ -13,8 +13,8 @@
 // operands, so one mask per two codes makes them (and a shift by 8 per four);
 // the factors 2^24 and 2^20 are powers of two that go into q and into the
 // output. q is bf16: its row is multiplied by a power of two that puts its
-// largest element at 2^14..2^15, so that its 8 significant bits fit for every
-// element within 2^38 of the largest. The weights p_j s_j are rounded to fp16 (half a step, 2^-11
+// largest element at 2^14..2^15, so that all its bits are kept for every
+// element within 2^27 of the largest. The weights p_j s_j are rounded to fp16 (half a step, 2^-11
 // relative; bf16 weights would add an error three times the output's own
 // rounding), scaled by a power of two that follows the largest s seen so far, so
 // that the largest is near 2^14 and small ones keep their bits.

@@ -331,7 +331,7 @@ extern "C" tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, 
   if (x_type != TERN_OUT_F32 && x_type != TERN_OUT_BF16) return TERN_EINVAL;
   const bool two = mode != TERN_NORM_PLAIN, add = mode == TERN_NORM_ADD;
   if (two && r_type != TERN_OUT_F32 && r_type != TERN_OUT_BF16) return TERN_EINVAL;
-  if (m < 0 || k < 1 || !(eps > 0.f) || ldx < k || ldq < k || (two && ldr < k) || (add && ldsum < k))
+  if (m < 0 || m > kMaxExtent || k < 1 || k > kMaxExtent || !(eps > 0.f) || ldx < k || ldq < k || (two && ldr < k) || (add && ldsum < k))
     return TERN_EINVAL;
   if (m == 0) return TERN_OK;
   if (!d_x || !d_gain || !d_xq || !d_xscale || (two && !d_r) || (add && !d_sum)) return TERN_EINVAL;

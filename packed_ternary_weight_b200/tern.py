@@ -485,6 +485,9 @@ class KV4Cache:
                 None if k is None else k.data_ptr(), ldk, None if v is None else v.data_ptr(), ldv)
 
     def attention_workspace_size(self, seqs: int, max_new: int, max_len: int, heads: int) -> int:
+        if 0 <= self.dev != _torch.cuda.current_device():  # planned for the multiprocessors of the cache's device
+            with _torch.cuda.device(self.dev):
+                return self.attention_workspace_size(seqs, max_new, max_len, heads)
         out = _sz()
         _check(lib.tern_kv4_attention_workspace_size(self._ref, seqs, max_new, max_len, heads, ctypes.byref(out)),
                "tern_kv4_attention_workspace_size")

@@ -56,6 +56,14 @@ def test_gemm_alignment_and_nothing_to_do():
     assert gemm(m=0, x=NULL, y=NULL, sx=NULL) == tern.OK
 
 
+def test_sizes_beyond_the_indices():
+    big = (1 << 30) + 1
+    for bad in (dict(m=big), dict(k=big, ldx=big, ldr=big, lds=big, ldq=big)):
+        assert norm(**bad) == tern.EINVAL
+    for bad in (dict(m=big), dict(n=big, ldy=big), dict(m=(1 << 31) - 1), dict(m=1 << 24, n=1 << 20, ldy=1 << 20)):
+        assert gemm(**bad) == tern.EINVAL
+
+
 def append(c=None, b=None, heads=20, type=1, q=P, ldq=2560, k=P, ldk=640, v=P, ldv=640, rope=P, max_pos=100, qo=P):
     c, b = c or cache(), b or batch()
     return tern.lib.tern_kv4_append(ctypes.byref(c), ctypes.byref(b), heads, type, q, ldq, k, ldk, v, ldv, rope, max_pos, qo, NULL)
