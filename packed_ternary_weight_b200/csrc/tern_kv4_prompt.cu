@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       const int stage = block & 1;
       const uint2 sp = pair;
       const float2 vp = __half22float2(as_half2(sp.y));
-      const bool bad_value = !(fabsf(vp.y) + 15.f * fabsf(vp.x) < 65520.f);  // as fp16, or not a number
+      const bool bad_value = !(fabsf(fmaf(15.f, vp.x, vp.y)) < 65520.f);  // beyond fp16, or not a number
       const uint32_t ab = __ballot_sync(0xffffffffu, cur.absent), po = __ballot_sync(0xffffffffu, bad_value);
       place(&nxt);
       slot = ahead.slot;
