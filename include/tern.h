@@ -497,7 +497,7 @@ tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32
  * own. Query head h reads kv head h / (heads / kv_heads); heads is a multiple of
  * kv_heads, any ratio. Products on fp16 operands with fp32 accumulation, the softmax
  * in fp32; q keeps all bits of every element within 2^27 of its row's largest. Sequences with up
- * to 16 new tokens x heads per kv head multiply by the codes, which are exact, and round
+ * to 48 new tokens x heads per kv head multiply by the codes, which are exact, and round
  * probabilities times value scales to fp16; longer ones round keys, values and
  * probabilities to fp16. Scores must be finite in fp32.
  *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.

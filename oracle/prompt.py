@@ -108,7 +108,7 @@ def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np
     The bound adds up: the bf16 rounding of the output, half a step 2^-8 of its value; the fp16 rounding of each
     probability times value scale, which weighs the code: 2^-11 sum p s c; and the fp32 accumulation, a few roundings
     of 2^-23 (the tensor cores may cut instead of round) of the sums of magnitudes, here and in the scores, whose
-    error d in the exponent changes every probability by d. Sequences of more than 16 query rows per kv head (with
+    error d in the exponent changes every probability by d. Sequences of more than 48 query rows per kv head (with
     `expanded` all) are computed from keys and values rounded to fp16, half a step 2^-11 of each element, and
     probabilities rounded to fp16."""
     d, kvh = cache.d, cache.kvh
@@ -137,7 +137,7 @@ def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np
                     out[starts[s] + i, h * g + e] = o
                     mag = abs(scale) * np.abs(qi).sum() * (15 * ks[:seen] + np.abs(km[:seen])).max()
                     err = 2.0 ** -20 * (mag + np.abs(sc).max() + 1)
-                    if expanded or n * g > 16:
+                    if expanded or n * g > 48:
                         err += 2.0 ** -11 * abs(scale) * np.abs(qi).sum() * np.abs(k[:seen]).max()
                         tol[starts[s] + i, h * g + e] += 1.01 * 2.0 ** -10 * (p @ np.abs(v[:seen]))
                     terms = p @ (np.abs(vm[:seen, None]) + vs[:seen, None] * vc[:seen])

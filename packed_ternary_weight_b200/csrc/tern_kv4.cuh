@@ -94,7 +94,13 @@ __device__ __forceinline__ bool find_share(int seqs, long long min_share, Weight
     total = scan(w, &incl);
     __syncthreads();
   }
-  const long long ctas = min((long long)gridDim.x, max(min(total, 1ll), total / min_share));
+  long long ctas = min((long long)gridDim.x, max(min(total, 1ll), total / min_share));
+  if (total > ctas && total <= 4 * ctas) {
+    // small shares: as few CTAs as leave the largest one as it is, so that fewer units are cut (8 sequences of 1000
+    // positions with 48 rows: 192 rounds on 96 CTAs 14 us, on 148 22 us; with shares of 14 rounds it cost 7 %)
+    const long long most = (total + ctas - 1) / ctas;
+    ctas = (total + most - 1) / most;
+  }
   if (blockIdx.x >= ctas) return false;
   out->total = total;
   out->ctas = ctas;

@@ -611,19 +611,22 @@ int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
   return launch_dependent(attn_kernel<D, NT>, ctas, kThreads, bytes, 1, s, p);
 }
 
-// How a batch within these bounds runs. Sequences of up to 16 query rows per kv
-// head take this file's kernel, 8 rows per CTA if no sequence has more, else 16;
-// longer ones the prompt kernel, whose 128-row tiles cost the same tensor time
-// from 17 rows on as from 128 but no more than the codes' expansion.
+// How a batch within these bounds runs. Sequences of up to 48 query rows per kv
+// head take this file's kernel, 8 rows per CTA if no sequence has more, else 16
+// (up to three tiles that read the codes anew, from L2); longer ones the prompt
+// kernel, whose time does not depend on the rows up to 256. At D = 128 with two kv
+// heads, this kernel with 16 / 32 / 48 rows and the prompt kernel: 64 sequences of
+// 4000 positions 38 / 61 / 85 and 94 us, one of 30000 23 / 23 / 26 and 59 us, 8 of 1000
+// 13 / 13 / 19 and 26 us; a fourth tile would lose.
 // Workspace: the CTAs' counters of both kernels, then their parts, at places that
 // only the device and the cache's shape decide, so that batches of any size share it.
 struct Plan {
   int rows, ctas;           // few rows: rows per CTA, CTAs; 0 if the batch has none
-  int prompt_ctas;          // 0 if no sequence may have more than 16 rows
+  int prompt_ctas;          // 0 if no sequence may have more than kMaxRows rows
   long long min_share;
   size_t part_off, prompt_off, total;
 };
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 48;
 
 tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int max_len, int sms, Plan* pl) {
   const long long rows = (long long)max_new * (heads / c.kv_heads);
@@ -632,17 +635,19 @@ tern_status plan_attn(const Kv4Params& c, int heads, int seqs, int max_new, int 
   // the kernels count rounds times CTAs in 64 bits
   if ((double)seqs * c.kv_heads * (double)((rows + 7) / 8) * (double)blocks > 1e15) return TERN_EUNSUPPORTED;
   pl->rows = rows <= 8 ? 8 : 16;
-  // one resident wave: two CTAs per multiprocessor with 8 rows, one with 16 (registers)
+  // one resident wave: two CTAs per multiprocessor with 8 rows, one with 16 (registers); no more than rounds
   const int wave = std::min(kMaxCtas, (pl->rows == 8 ? 2 : 1) * sms), prompt_wave = std::min(kMaxCtas, sms);
-  pl->ctas = (int)std::min<double>(wave, std::max(1.0, (double)seqs * c.kv_heads * 2 * (double)rounds));
+  pl->ctas = (int)std::min<double>(wave, std::max(1.0, (double)seqs * c.kv_heads * (kMaxRows / 16) * (double)rounds));
   pl->prompt_ctas = 0;
   if (rows > kMaxRows) {
     pl->prompt_ctas = prompt_wave;
     if (seqs == 1) pl->ctas = 0;  // the prompt kernel takes the one sequence whatever its length
   }
-  // a CTA of the prompt kernel takes four blocks or more, and no unit is cut
-  // into more than about 16 parts, which its last CTA reads
-  pl->min_share = std::max(4ll, blocks / 16);
+  // Blocks that a CTA of the prompt kernel takes at least: a unit's last CTA reads all its parts, so up to 8 parts
+  // of fewer than four blocks and 16 of more. 64 tokens, 4 kv heads, of 64 / 4000 / 16000 / 60000 positions: 13 / 33 /
+  // 63 / 112 us (never fewer than four blocks: 39 us at 64; up to 8 parts always: 175 us at 60000; up to 32: 62, 78 and
+  // 107 us at the last three)
+  pl->min_share = std::max({1ll, std::min(4ll, blocks / 8), blocks / 16});
   const size_t slot8 = (size_t)8 * (size_t)(c.dim + 2) * 4;
   pl->part_off = 2 * kMaxCtas * sizeof(unsigned);
   // 2 wave slots of 8 rows or wave slots of 16: the same size

@@ -268,10 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.misc[tc::kMiscTmem], 0);
   Walk walk(p, sh);
   Segment g;
-  // the waits of whole warps: suspended by the hardware, bounded, given up at once after another's expiry
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!misc[tc::kMiscAbort] && !mbar_wait_bounded(bar, parity)) misc[tc::kMiscAbort] = 1u;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { tc::tc_wait_late<true>(bar, parity, misc); };
 
   // The 768 threads start with 80 registers each, the whole file. Shares per
   // group of four warps: 4 x 88 (softmax) + 88 + 40 = 6 x 80.
@@ -625,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       const uint32_t lead = lane == 0 ? 1u : 0u;
       bool ok = true;
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, tc::tc_wait(bar, parity, misc)) && ok;
+        ok = __all_sync(0xffffffffu, tc::tc_wait_late<false>(bar, parity, misc)) && ok;
       };
       uint32_t block = 0, p_ph[2] = {0, 0}, q_ph[2] = {0, 0}, o_uses[2] = {0, 0};
       // descriptors: an address offset adds to the field in units of 16 bytes

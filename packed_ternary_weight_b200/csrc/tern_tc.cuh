@@ -328,6 +328,27 @@ __device__ __forceinline__ bool tc_wait_many(uint64_t* bar, uint32_t parity, vol
   }
 }
 
+// Bounded wait that reads the clock only after many tests: that read takes longer than most waits last. Polling, or
+// (kSuspend, for roles of many warps) suspended by the hardware between tests.
+template <bool kSuspend>
+__device__ __forceinline__ bool tc_wait_late(uint64_t* bar, uint32_t parity, volatile uint32_t* misc) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (kSuspend ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+    if ((it & 255u) == 0u) {
+      if (misc[kMiscAbort]) return false;
+      if (it == 0u) continue;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        atomicOr(&g_dev_error, TERN_DEVERR_TIMEOUT);
+        misc[kMiscAbort] = 1u;
+        return false;
+      }
+    }
+  }
+}
+
 // tc_wait for phases that the other CTA's threads complete.
 __device__ __forceinline__ bool tc_wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* misc) {
   const uint64_t t0 = global_timer_ns();
