@@ -49,6 +49,7 @@ constexpr int kBytesA = kRowsA * kStepK;  // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;
 constexpr int kMinSteps = 4;              // of K for each CTA of a split tile
+constexpr int kTileCost = 64, kPairCost = 32;  // of a tile beyond its tokens, in tokens
 constexpr int kSmemTop = 227 * 1024;
 
 struct Plan {
@@ -344,20 +345,40 @@ const int* resident_clusters(int sms) {
   return t;
 }
 
-// Tokens per tile: the fewest tiles of up to 256, of equal size. Pairs of CTAs
-// from one 256-channel tile per pair of SMs on. Fewer tiles than SMs: split K over
-// a cluster, as long as every CTA keeps four steps; of the cluster sizes the one
-// with the least steps in a row, where meeting costs about four.
+// Tokens per tile: up to 256, so that the waves of tiles cost least, a tile its
+// tokens and a constant for its weights (2000 x 2560 x 2560: 13 times 160 tokens,
+// two waves, 19 us; the fewest tiles, 8 of 256, 27 us. 4095 x 2560 x 2560 33 and 40 us.
+// Constants from 64 to 160 differ by 3 %). Pairs of CTAs from one 256-channel tile
+// per pair of SMs on and with wide tiles (256 x 32768 x 2560: pairs 31.5, single CTAs
+// 33.4 us; 4095 x 14336 x 4096 202 and 220; 128 x 32768 x 2560 22.7 and 21.7).
+// Fewer tiles than half the SMs: the fewest, and K split over a cluster, as long as
+// every CTA keeps four steps; of the cluster sizes the one with the least steps in a
+// row, where meeting costs about four (61 x 2560 x 6912: 7 us, unsplit 16 us).
 Plan make_plan(int m, int n, int k, int sms) {
   Plan pl{};
-  pl.tiles_m = (m + 255) / 256;
-  const long long pair_tiles = (long long)((n + 2 * kRowsA - 1) / (2 * kRowsA)) * pl.tiles_m;
-  pl.pair = m > 64 && pair_tiles >= sms / 2;
-  const int unit = pl.pair ? 32 : 16, rows = pl.pair ? 2 * kRowsA : kRowsA;
-  pl.tn = ((m + pl.tiles_m - 1) / pl.tiles_m + unit - 1) / unit * unit;
-  pl.tiles_m = (m + pl.tn - 1) / pl.tn;
-  pl.tiles_n = (n + rows - 1) / rows;
   pl.steps = (k + kStepK - 1) / kStepK;
+  // one CTA per tile, then pairs; from the fewest tiles to twice as many
+  double best = 0;
+  auto consider = [&](int pair) {
+    const int unit = pair ? 32 : 16, rows = pair ? 2 * kRowsA : kRowsA, units = pair ? sms / 2 : sms;
+    const int tiles_n = (n + rows - 1) / rows, fewest = (m + 255) / 256;
+    for (int t = fewest; t <= fewest + std::min(fewest, 16); ++t) {
+      const int tn = ((m + t - 1) / t + unit - 1) / unit * unit;
+      if (tn > 256) continue;
+      const long long tiles = (long long)tiles_n * ((m + tn - 1) / tn);
+      if (pair ? tn <= 208 || tiles < units : t > fewest && tiles <= units / 2) continue;
+      const double cost = (double)((tiles + units - 1) / units) * (tn + (pair ? kPairCost : kTileCost));
+      if (best != 0 && cost >= best) continue;
+      best = cost;
+      pl.pair = pair;
+      pl.tn = tn;
+      pl.tiles_n = tiles_n;
+      pl.tiles_m = (m + tn - 1) / tn;
+      if (!pair && t == fewest && tiles <= units / 2) return;  // K is split instead
+    }
+  };
+  consider(0);
+  consider(1);
   const long long tiles = (long long)pl.tiles_n * pl.tiles_m;
   pl.tiles = (int)tiles;
   pl.split = 1;
