@@ -6,10 +6,12 @@
 // A group of D / 16 lanes takes one (token, head) at a time: lane l holds the
 // dimensions 8l .. 8l + 7 and D/2 + 8l .. + 7, the pairs that rotate_half combines,
 // so the rotation needs no exchange, bf16 rows are read in 16-byte pieces and each
-// lane's codes are two whole words. Minimum and maximum go over the group by shuffles. A warp takes one
-// head per group of a few tokens and up to three of each of many: the search for
-// the token's sequence, its rotation row and its page are then shared by them,
-// and the heads' loads are issued together, ahead of that search.
+// lane's codes are two whole words. Minimum and maximum go over the group by
+// shuffles. A warp takes one head per group of a few tokens and up to three of each
+// of many: the search for the token's sequence, its rotation row and its page are
+// then shared by them, and the heads' loads are issued together, ahead of that search.
+// 8813 prompt tokens (32 heads on 8 kv heads, D = 128, bf16): append 40 us, 3.9 TB/s,
+// bound by instruction issue (59 % of the slots) next to memory; read 13.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -247,7 +249,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Kv4ReadParams p) {
     void* dst = is_k ? p.k : p.v;
     if (!dst) continue;
     const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pair[i]));
-    T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)(is_k ? g : g - c.kv_heads) * D + 8 * gl;
+    T* out = static_cast<T*>(dst) + (int64_t)t * (is_k ? p.ldk : p.ldv) + (size_t)(is_k ? g : g - c.kv_heads) * D +
+             8 * gl;
     // scale * code is exact in fp32 (11 + 4 bits), so the fused form rounds once, as the definition
     float a[8], b[8];
 #pragma unroll

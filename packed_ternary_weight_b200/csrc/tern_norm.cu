@@ -3,7 +3,7 @@
 // a layer (QORA-LLM-2B page, "SubLN Pattern (4 norms per layer)"), for many
 // rows. The values are those of the decode step's normalisations:
 //   f = fl32(1 / sqrt(mean(v^2) + eps)), the sum and the root in fp64 (each
-//   v^2 is exact there, so the order of the sum does not show in f);
+//   v^2 is exact there, and sums in any order agree far below f's own rounding);
 //   y = fl32(fl32(v f) gain); a = max |y|; q = clamp(rint(fl32(y fl32(127 / a))), -127, 127).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -331,7 +331,8 @@ extern "C" tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, 
   if (x_type != TERN_OUT_F32 && x_type != TERN_OUT_BF16) return TERN_EINVAL;
   const bool two = mode != TERN_NORM_PLAIN, add = mode == TERN_NORM_ADD;
   if (two && r_type != TERN_OUT_F32 && r_type != TERN_OUT_BF16) return TERN_EINVAL;
-  if (m < 0 || m > kMaxExtent || k < 1 || k > kMaxExtent || !(eps > 0.f) || ldx < k || ldq < k || (two && ldr < k) || (add && ldsum < k))
+  if (m < 0 || m > kMaxExtent || k < 1 || k > kMaxExtent || !(eps > 0.f) || ldx < k || ldq < k ||
+      (two && ldr < k) || (add && ldsum < k))
     return TERN_EINVAL;
   if (m == 0) return TERN_OK;
   if (!d_x || !d_gain || !d_xq || !d_xscale || (two && !d_r) || (add && !d_sum)) return TERN_EINVAL;
