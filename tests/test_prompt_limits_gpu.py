@@ -88,3 +88,22 @@ def test_calls_of_every_kind_at_once(tern):
     for (_, out), w in zip(calls, want):
         assert torch.equal(out, w)
     assert tern.device_error() == tern.OK
+
+
+@pytest.mark.parametrize("group", [1, 4, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_at_the_border_of_the_kernels(tern, group, d):
+    # 48 query rows per kv head and one token more, beside single tokens; in place as well
+    from tests import prompt_util as u
+    n = 48 // group
+    b = u.Batch([n, n + 1, 1, n], [600, 300, 520, n], 2, d, 32, seed=group)
+    b.fill_values()
+    heads, scale = 2 * group, d ** -0.5
+    q = u.bf16_dev(b.g.standard_normal((b.rows, heads * d)))
+    cache, batch = b.device()
+    out, ws = torch.empty_like(q), u.workspace(cache, heads, 4, n + 1, 600)
+    cache.attention(batch, q, scale, out, ws)
+    ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, heads, scale, q.float().cpu().numpy().reshape(-1, heads, d))
+    assert (np.abs(out.float().cpu().numpy().reshape(ref.shape) - ref) <= tol).all()
+    cache.attention(batch, q, scale, q, ws)
+    assert torch.equal(q, out) and tern.device_error() == tern.OK
