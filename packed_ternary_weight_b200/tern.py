@@ -289,11 +289,12 @@ _OUT_TYPE: dict = {}
 
 def _import_torch():
     """torch, imported on first use (packing needs none); its types as TERN_OUT_*."""
-    global _torch, _current_stream
+    global _torch, _current_stream, _current_device
     import torch
     _OUT_TYPE.update({torch.float32: OUT_F32, torch.bfloat16: OUT_BF16})
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda dev: torch.cuda.current_stream(dev).cuda_stream)  # the handle alone costs a tenth of the object
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return torch
 
@@ -309,8 +310,10 @@ def _type(t, what: str) -> int:
 
 
 def _rows(t, shape, what: str) -> int:
-    """Row stride of a tensor of shape (m, k) whose rows are contiguous."""
-    if t.shape != shape or len(shape) != 2:
+    """Row stride of a tensor of the shape (m, k) whose rows are contiguous."""
+    if t.is_contiguous() and t.shape == shape:  # most calls
+        return shape[1]
+    if t.shape != shape:
         _bad(what)
     ld, one = t.stride()
     m, k = shape
@@ -328,9 +331,8 @@ def _launch(dev: int, stream, what: str, fn, *args):
     """Call an entry point on the device that the tensors are on (their get_device())."""
     if dev < 0:
         _bad(f"{what}: tensors are not on a CUDA device")
-    cuda = _torch.cuda
-    if dev != cuda.current_device():
-        with cuda.device(dev):
+    if dev != _current_device():
+        with _torch.cuda.device(dev):
             return _launch(dev, stream, what, fn, *args)
     code = fn(*args, _current_stream(dev) if stream is None else _stream(stream))
     if code != OK:
