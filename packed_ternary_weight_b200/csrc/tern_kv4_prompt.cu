@@ -34,14 +34,15 @@
 // between CTAs is joined by the last of them, in position order.
 //
 // Measured: 2048-token chunks behind 6142 positions and shorter ones (32 heads on 8 kv
-// heads, D = 128) 0.44 ms, 0.86 PFLOP/s, half of the measured bf16 rate. A block of both
+// heads, D = 128) 0.43 ms, 0.88 PFLOP/s, half of the measured bf16 rate. A block of both
 // tiles takes about 4800 cycles, 2050 of them of tensor work at the full rate; the limit is
 // each tile's own chain, which nothing shortens by overlap: softmax 2700 (its exponentials
 // alone 2050 of the special-function pipe, shared with the other tile), O += P V and the
 // next S 1400 (S takes 95 instead of 64 cycles per instruction: both operands come from
 // shared memory), and the signals between the roles 700. Without gain were: 64-position
 // halves with two score buffers, probabilities handed over in halves, one reading of the
-// scores, a polynomial for a part of the exponentials, eight instead of four expanding warps.
+// scores, a polynomial for a part of the exponentials, eight instead of four expanding
+// warps; three idle warps for register shares of 88 (softmax, expansion) and 40 cost 2 %.
 // Every wait is bounded; on expiry the device error word records a timeout and the
 // CTA runs to its end without waiting further.
 #include <cuda_bf16.h>
@@ -63,7 +64,7 @@ namespace {
 using kv4::ex2;
 using kv4::exp2i;
 
-constexpr int kWarps = 24;  // of them 21-23 idle: register shares move between groups of four warps
+constexpr int kWarps = 21;
 constexpr int kExpandWarp = 16, kMmaWarp = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlock = 128;             // positions
@@ -280,11 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
   Segment g;
   auto wait = [&](uint64_t* bar, uint32_t parity) { tc::tc_wait_late<true>(bar, parity, misc); };
 
-  // The 768 threads start with 80 registers each, the whole file. Shares per
-  // group of four warps: 4 x 88 (softmax) + 88 + 40 = 6 x 80.
   if (warp < kExpandWarp) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     const int x = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127, pair = 1 + 4 * x + (warp & 3);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)(128 * x + 64 * half),
@@ -539,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- codes -> operands
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
     // Three steps in flight: the page of block i + 2, the codes of block i + 1, block i into shared memory.
     const int tid = threadIdx.x - 32 * kExpandWarp;  // position within a block
     struct {
@@ -626,7 +623,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     }
   } else {
     // ------------------------------------------------------------------ MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kMmaWarp) {
       // the whole warp in step, one lane of it issuing
       constexpr uint32_t id_s = tc::idesc_f16_f32(kBlock, false), id_o = tc::idesc_f16_f32(D, true);
