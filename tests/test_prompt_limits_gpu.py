@@ -107,3 +107,22 @@ def test_rows_at_the_border_of_the_kernels(tern, group, d):
     assert (np.abs(out.float().cpu().numpy().reshape(ref.shape) - ref) <= tol).all()
     cache.attention(batch, q, scale, q, ws)
     assert torch.equal(q, out) and tern.device_error() == tern.OK
+
+
+def test_prompts_among_many_sequences(tern):
+    # more sequences than a CTA has threads: the search for a share goes over them in turns
+    from tests import prompt_util as u
+    new = [1] * 800
+    length = [1 + s % 5 for s in range(800)]
+    for s, n in ((3, 60), (400, 130), (671, 49), (672, 70), (799, 50)):
+        new[s], length[s] = n, n + 7 * (s % 4)
+    new[10] = new[700] = length[10] = 0
+    b = u.Batch(new, length, 1, 64, 16, seed=8)
+    b.fill_values()
+    q = u.bf16_dev(b.g.standard_normal((b.rows, 64)))
+    cache, batch = b.device()
+    out = torch.empty_like(q)
+    cache.attention(batch, q, 0.125, out, u.workspace(cache, 1, 800, 130, max(length)))
+    ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, 1, 0.125, q.float().cpu().numpy().reshape(-1, 1, 64))
+    assert (np.abs(out.float().cpu().numpy().reshape(ref.shape) - ref) <= tol).all()
+    assert tern.device_error() == tern.OK
