@@ -496,10 +496,12 @@ tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32
  * already): out = softmax(scale q k^T) v over the positions up to the token's
  * own. Query head h reads kv head h / (heads / kv_heads); heads is a multiple of
  * kv_heads, any ratio. Products on fp16 operands with fp32 accumulation, the softmax
- * in fp32; q keeps all bits of every element within 2^27 of its row's largest. Sequences with up
+ * in fp32; q keeps all bits of every element within 2^27 of its row's largest (elements
+ * below 2^-127 excepted). Sequences with up
  * to 48 new tokens x heads per kv head multiply by the codes, which are exact, and round
  * probabilities times value scales to fp16; longer ones round keys, values and
- * probabilities to fp16. Scores must be finite in fp32.
+ * probabilities to fp16. Scores must be finite in fp32, and scale times any element
+ * of q below 2^117.
  *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.
  */
 tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, float scale,

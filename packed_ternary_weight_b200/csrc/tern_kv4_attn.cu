@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
       for (int j = 0; j < NT; ++j) {
         const int row = row_first + 8 * j + r, tok = row / G;
         uint4 u[KW];
-        float sum = 0.f, big = 0.f;
+        float sum = 0.f, big = 0.f;  // the sum of the scaled row, which stays in range whatever its size
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           u[w] = make_uint4(0, 0, 0, 0);
@@ -420,12 +420,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float x = __uint_as_float(e[i] << 16), y = __uint_as_float(e[i] & 0xFFFF0000u);
-            sum += x + y;
             big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
           }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const int ex = max(-100, (__float_as_int(big) >> 23) - 127);  // exponent of the largest element
@@ -439,16 +436,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
           for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(e[i] << 16);
             v[2 * i + 1] = __uint_as_float(e[i] & 0xFFFF0000u);
+            sum += v[2 * i] * fe + v[2 * i + 1] * fe;
           }
           S.qf[j][2 * w][0] = pack_half2(v[0] * fe, v[4] * fe);
           S.qf[j][2 * w][1] = pack_half2(v[1] * fo, v[5] * fo);
           S.qf[j][2 * w + 1][0] = pack_half2(v[2] * fe, v[6] * fe);
           S.qf[j][2 * w + 1][1] = pack_half2(v[3] * fo, v[7] * fo);
         }
-        const float back = exp2i(min(127, 24 - 14 + ex)) * p.scale_log2;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        // the row's exponent meets the scale first: a large row has a small scale, and neither product leaves fp32
+        const float unit = exp2i(ex) * p.scale_log2, back = unit * 1024.f;  // 2^(ex - 14 + 24) scale
+        sum *= unit * 0x1p-14f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          S.sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4) * p.scale_log2;
+          S.sumq[j][e] = __shfl_sync(0xffffffffu, sum, (2 * t + e) * 4);
           S.rowf[j][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
           const int rw = row_first + 8 * j + 2 * t + e;
           S.lim[j][e] = rw < rows ? min(end, q.len - q.n + rw / G + 1) : 0;
