@@ -106,9 +106,10 @@ def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np
     """Outputs fp64 [tokens][heads][d] and a bound on how far the kernel's may be from them.
 
     The bound adds up: the bf16 rounding of the output, half a step 2^-8 of its value; the fp16 rounding of each
-    probability times value scale, which weighs the code: 2^-11 sum p s c; and the fp32 accumulation, a few roundings
-    of 2^-23 (the tensor cores may cut instead of round) of the sums of magnitudes, here and in the scores, whose
-    error d in the exponent changes every probability by d. Sequences of more than 48 query rows per kv head (with
+    probability times value scale w = p s, which enters as w c + p (m + 7.5 s) - 7.5 w and so weighs the code's distance
+    from 7.5: 2^-11 sum p s |c - 7.5|; and the fp32 accumulation, a few roundings of 2^-23 (the tensor cores may cut
+    instead of round) of the sums of magnitudes |m| + s c + 15 s, here and in the scores, whose error d in the exponent
+    changes every probability by d. Sequences of more than 48 query rows per kv head (with
     `expanded` all) are computed from keys and values rounded to fp16, half a step 2^-11 of each element, and
     probabilities rounded to fp16."""
     d, kvh = cache.d, cache.kvh
@@ -140,8 +141,9 @@ def attention(cache: Cache, table, starts, lens, heads: int, scale: float, q: np
                     if expanded or n * g > 48:
                         err += 2.0 ** -11 * abs(scale) * np.abs(qi).sum() * np.abs(k[:seen]).max()
                         tol[starts[s] + i, h * g + e] += 1.01 * 2.0 ** -10 * (p @ np.abs(v[:seen]))
-                    terms = p @ (np.abs(vm[:seen, None]) + vs[:seen, None] * vc[:seen])
-                    tol[starts[s] + i, h * g + e] += (2.0 ** -8 * np.abs(o) + 1.01 * 2.0 ** -11 * (p @ (vs[:seen, None] * vc[:seen]))
+                    terms = p @ (np.abs(vm[:seen, None]) + vs[:seen, None] * (vc[:seen] + 15))
+                    off = p @ (vs[:seen, None] * np.abs(vc[:seen] - 7.5))
+                    tol[starts[s] + i, h * g + e] += (2.0 ** -8 * np.abs(o) + 1.01 * 2.0 ** -11 * off
                                                      + 2 * err * (p @ np.abs(v[:seen]) + np.abs(o)) + 2.0 ** -20 * terms)
     return out, tol
 

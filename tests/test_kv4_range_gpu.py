@@ -51,3 +51,21 @@ def test_queries_at_the_top_of_the_range(tern, d, new, heads, kind):
     q, got = attend(tern, b, heads, scale, q * 2.0 ** 121)
     ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, heads, scale, q)
     assert (np.abs(got - ref) <= tol).all(), float(np.nanmax(np.abs(got - ref) / tol))
+
+
+@pytest.mark.parametrize("new", [1, 3])
+@pytest.mark.parametrize("d,length", [(64, 500), (128, 900)])
+def test_roundings_of_the_weights_cancel_in_the_offset(tern, new, d, length):
+    # Values of codes 7 and 8 about zero, and weights that are all alike but for one position in 32, so that all of them
+    # are rounded the same way: the offset 7.5 scale, fifteen times the values, must not bring that rounding in.
+    b = util().Batch([new], [length], 1, d, 16, seed=42)
+    c, heads = b.oracle_cache(), 8
+    for j in range(length):
+        at = (int(b.table[0, j // 16]), j % 16, 0)
+        c.put(*at, 0, np.zeros(d, np.uint8), np.float16(0), np.float16(j % 32 == 0))
+        c.put(*at, 1, b.g.integers(7, 9, d).astype(np.uint8), np.float16(0.75), np.float16(-5.625))
+    q = np.zeros((new, heads, d))
+    q += np.linspace(0.07, 0.95, new * heads).reshape(new, heads, 1) / d   # the others' weight is 2^-(that)
+    q, got = attend(tern, b, heads, math.log(2.0), q)
+    ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, heads, math.log(2.0), q)
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
