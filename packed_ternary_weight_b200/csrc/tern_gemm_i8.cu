@@ -177,15 +177,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // no load may be under way when the CTA ends (the odd CTA of a pair waits for the even one below)
-      if (misc[tc::kMiscAbort] && (!PAIR || rank == 0)) {
-        for (int i = 0; i < min(issued, pl.stages); ++i) {
-          if (--stage < 0) {
-            stage = pl.stages - 1;
-            ph ^= 1u;
-          }
-          mbar_wait_bounded(&ctl.full[stage], ph);
+      // When the CTA ends, no load may be under way (the odd CTA of a pair waits for the even one below), and in the odd
+      // CTA no signal of the even one's MMAs, which may come after its last thread has nothing left to do.
+      const bool gave_up = misc[tc::kMiscAbort], odd = PAIR && rank == 1;
+      for (int i = 0; gave_up != odd && i < min(issued, pl.stages); ++i) {
+        if (--stage < 0) {
+          stage = pl.stages - 1;
+          ph ^= 1u;
         }
+        if (!mbar_wait_bounded(odd ? &ctl.empty[stage] : &ctl.full[stage], ph) && odd) break;
       }
     }
   } else if (warp == 1 && (!PAIR || rank == 0)) {
@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every MMA issued has completed before tensor memory is released
     PAIR ? tc::commit_pair(&ctl.fin, lead) : tc::commit_lead(&ctl.fin, lead);
     mbar_wait_bounded(&ctl.fin, 0u);
+  } else if (warp == 1) {
+    mbar_wait_bounded(&ctl.fin, 0u);  // the odd CTA's copy: all that the even one sends here has come
   } else if (warp >= 4) {
     const int q4 = warp & 3, et = threadIdx.x - 128;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
@@ -265,8 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if constexpr (PAIR) {  // neither CTA's shared memory, barriers or tensor memory go before the other is done
-    cluster_arrive_relaxed();
+  if constexpr (PAIR) {  // neither CTA's shared memory, barriers or tensor memory go before the other is done: its
+                         // arrivals on them are released here, and the MMAs' have been waited for above
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     cluster_wait_acquire();
   }
   if (!PAIR && pl.split > 1) {
