@@ -391,8 +391,9 @@ typedef enum { TERN_NORM_PLAIN = 1, TERN_NORM_ADD = 2, TERN_NORM_RELU2 = 3 } ter
  *   v = fl(fl(g g) r), g = max(x, 0)    (TERN_NORM_RELU2)
  *   y_i = fl(fl(v_i f) gain_i), f = fl(1 / sqrt(mean(v^2) + eps)) (sum in fp64)
  *   xq, xscale = the rule of tern_quantize_act on y
- * the same values as the normalisations inside tern_decode_step. Inputs must be
- * finite. m = 0 does nothing.
+ * the same values as the normalisations inside tern_decode_step. A row in which
+ * some v, f or y is not finite has codes 0 and a scale that is not finite, so that
+ * what is computed from it is not either. m = 0 does nothing.
  *   d_x [m][k] of x_type (TERN_OUT_F32 or TERN_OUT_BF16), row stride ldx >= k;
  *   d_r [m][k] of r_type, ldr >= k (TERN_NORM_PLAIN: ignored);
  *   d_gain fp32 [k]; eps > 0;

@@ -5,6 +5,7 @@
 //   f = fl32(1 / sqrt(mean(v^2) + eps)), the sum and the root in fp64 (each
 //   v^2 is exact there, and sums in any order agree far below f's own rounding);
 //   y = fl32(fl32(v f) gain); a = max |y|; q = clamp(rint(fl32(y fl32(127 / a))), -127, 127).
+// A row in which some v, f or y is not finite has a scale that is not finite, and codes 0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,6 +22,12 @@ __device__ __forceinline__ float ld1(const float* p) { return *p; }
 __device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// The larger one, not a number if either is not: a row's maximum must show what stands in the row.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float round_to(float v, const float*) { return v; }
 __device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) {
   return __bfloat162float(__float2bfloat16_rn(v));
@@ -30,7 +37,7 @@ template <int MODE, typename RT>
 __device__ __forceinline__ float combine(float x, float r) {
   if constexpr (MODE == TERN_NORM_ADD) return round_to(__fadd_rn(x, r), static_cast<const RT*>(nullptr));
   if constexpr (MODE == TERN_NORM_RELU2) {
-    const float g = fmaxf(x, 0.f);
+    const float g = max_nan(x, 0.f);
     return __fmul_rn(__fmul_rn(g, g), r);
   }
   return x;
@@ -59,13 +66,13 @@ __device__ __forceinline__ float row_factor(double ss, int k, float eps, double*
 }
 __device__ __forceinline__ float row_max(float a, float* red) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = 16; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
   __syncthreads();
   const int warps = blockDim.x >> 5;
   a = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = 16; o; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
 }
 
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
     return __fmul_rn(__fmul_rn(v, f), p.gain[i]);
   };
   float a = 0.f;
-  for (int i = threadIdx.x; i < k; i += blockDim.x) a = fmaxf(a, fabsf(y(i)));
+  for (int i = threadIdx.x; i < k; i += blockDim.x) a = max_nan(a, fabsf(y(i)));
   a = row_max(a, redf);
   const float inv = a > 0.f ? __fdiv_rn(127.0f, a) : 0.f;
   int8_t* q = p.xq + (int64_t)row * p.ldq;
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const NormParams p) {
     const float v = y(i);
     q[i] = v != 0.f ? quant(v, inv) : (int8_t)0;
   }
-  if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : 0.f;
+  if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : a;
 }
 
 // Two fp32 operations in one instruction, each rounded as its own (only where no
@@ -171,7 +178,7 @@ __device__ __forceinline__ float2 combine2(float2 x, float2 r) {
     return make_float2(round_to(v.x, static_cast<const RT*>(nullptr)), round_to(v.y, static_cast<const RT*>(nullptr)));
   }
   if constexpr (MODE == TERN_NORM_RELU2) {
-    const float2 g = make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f));
+    const float2 g = make_float2(max_nan(x.x, 0.f), max_nan(x.y, 0.f));
     return mul2(mul2(g, g), r);
   }
   return x;
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[j][e] = mul2(mul2(v[j][e], f2), gain[e]);
-          a = fmaxf(a, fmaxf(fabsf(v[j][e].x), fabsf(v[j][e].y)));
+          a = max_nan(a, max_nan(fabsf(v[j][e].x), fabsf(v[j][e].y)));
         }
       }
     }
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p
         if (first + j * step < k)
           *reinterpret_cast<uint2*>(out + j * step) = make_uint2(word(v[j][0], v[j][1]), word(v[j][2], v[j][3]));
     };
-    if (inv != INFINITY) {
+    if (inv > 0.f && inv != INFINITY) {
       // |y| <= a, so |y inv| is at most 127 (1 + 2^-22): the sum with 1.5 * 2^23 rounds it to the integer (ties to
       // even) that its low byte holds, and no clamp is needed
       // (one by one: the packed product and sum are contracted into one rounding)
@@ -257,11 +264,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p
       store([&](float2 x, float2 y) {
         return __byte_perm(__byte_perm(low(x.x), low(x.y), 0x0040), __byte_perm(low(y.x), low(y.y), 0x0040), 0x5410);
       });
-    } else {  // a tiny row takes the definition's steps
+    } else {  // a tiny row takes the definition's steps, and one that is empty or not finite gets zeros
       auto q = [&](float y) { return (uint32_t)(y != 0.f ? quant(y, inv) : 0) & 0xFFu; };
       store([&](float2 x, float2 y) { return q(x.x) | (q(x.y) << 8) | (q(y.x) << 16) | (q(y.y) << 24); });
     }
-    if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : 0.f;
+    if (threadIdx.x == 0) p.xscale[row] = a > 0.f ? __fdiv_rn(a, 127.0f) : a;
   }
 }
 
