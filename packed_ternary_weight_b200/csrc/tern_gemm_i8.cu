@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = (tile % pl.tiles_n) * kRowsTile + n_off + 32 * q4 + lane, m0 = (tile / pl.tiles_n) * pl.tn;
       const int cols = min(pl.tn, p.m - m0);
       float* sx = ctl.sx[buf];
-      for (int i = et; i < cols; i += 128) sx[i] = __ldg(p.xscale + m0 + i);
-      const float sw = n < p.n ? __ldg(p.wscale + n) : 0.f;
+      for (int i = et; i < cols; i += 128) sx[i] = p.xscale[m0 + i];
+      const float sw = n < p.n ? p.wscale[n] : 0.f;
       named_sync_epilogue();
       tc::tc_wait_many(&ctl.acc_full[buf], (uint32_t)(seg / 2) & 1u, misc);
       tc::fence_after_sync();
@@ -283,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n < p.n) {
       float sw[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sw[i] = n + i < p.n ? __ldg(p.wscale + n + i) : 0.f;
+      for (int i = 0; i < 4; ++i) sw[i] = n + i < p.n ? p.wscale[n + i] : 0.f;
       for (int c = rank + pl.split * (int)(threadIdx.x >> 5); c < cols; c += 8 * pl.split) {
         const uint32_t at = ring + (uint32_t)(c * kRowsA + 4 * (int)(threadIdx.x & 31)) * 4u;
-        const float sx = __ldg(p.xscale + m0 + c);
+        const float sx = p.xscale[m0 + c];
         int4 v[kMaxSplit];
 #pragma unroll
         for (int r = 0; r < kMaxSplit; ++r)

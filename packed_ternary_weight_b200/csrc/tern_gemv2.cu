@@ -150,7 +150,7 @@ __device__ void stage_x_int8(const Gemv2Params& p, const Gemv2Problem& pr, const
     if (t < m) {
       const int8_t* src = x + (size_t)t * K + k;
       if (p.x_vec && k + 16 <= K) {
-        v = __ldg(reinterpret_cast<const uint4*>(src));
+        v = *reinterpret_cast<const uint4*>(src);
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -198,7 +198,7 @@ __device__ void stage_x_q8(const Gemv2Params& p, const Gemv2Problem& pr, const S
     if (t < m) {
       const uint16_t* src = x + (size_t)t * K + k;
       if (p.x_vec && k + 8 <= K) {
-        v = __ldg(reinterpret_cast<const uint4*>(src));
+        v = *reinterpret_cast<const uint4*>(src);
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll

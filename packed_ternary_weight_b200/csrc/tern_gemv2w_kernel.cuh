@@ -129,7 +129,7 @@ __device__ __forceinline__ float bf16_abs_max8(uint4 v) {
 
 // Eight bf16 values x[k .. k+8) (zero beyond K) as one 16-byte vector.
 __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* x, int K, int k, bool vec) {
-  if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(x + k));
+  if (vec && k + 8 <= K) return *reinterpret_cast<const uint4*>(x + k);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -139,7 +139,7 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* x, int K, int k, bo
 
 // Sixteen int8 values x[k .. k+16) (zero beyond K).
 __device__ __forceinline__ uint4 load_s8x16(const int8_t* x, int K, int k, bool vec) {
-  if (vec && k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(x + k));
+  if (vec && k + 16 <= K) return *reinterpret_cast<const uint4*>(x + k);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 16; ++j)

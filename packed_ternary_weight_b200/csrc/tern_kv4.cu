@@ -30,11 +30,11 @@ constexpr int kThreads = 256;
 // all lanes of a warp together, 32 candidates a round; -1 for a row outside.
 __device__ __forceinline__ int seq_of(const Kv4Params& c, int t) {
   int lo = 0, n = c.seqs + 1;  // candidates lo .. lo + n - 1 among start[0 .. seqs]
-  if (__ldg(c.start) > t) return -1;
+  if (c.start[0] > t) return -1;
   while (n > 1) {
     const int step = (n + 31) >> 5;
     const int i = lo + (int)(threadIdx.x & 31) * step;
-    const bool le = i < lo + n && __ldg(c.start + i) <= t;
+    const bool le = i < lo + n && c.start[i] <= t;
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
     const int next = lo + last * step;
     n = min(step, lo + n - next);
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
     const float4* row = reinterpret_cast<const float4*>(p.rope + ((size_t)pos * (D / 2) + 8 * gl) * 2);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 cs = __ldg(row + k);
+      const float4 cs = row[k];
       co[2 * k] = cs.x, si[2 * k] = cs.y, co[2 * k + 1] = cs.z, si[2 * k + 1] = cs.w;
     }
   }

@@ -17,8 +17,8 @@ struct Seq {
 // reported in the device error word and the sequence left out.
 __device__ __forceinline__ Seq load_seq(const Kv4Params& c, int s) {
   Seq q;
-  const int a = __ldg(c.start + s), b = __ldg(c.start + s + 1);
-  q.len = __ldg(c.len + s);
+  const int a = c.start[s], b = c.start[s + 1];
+  q.len = c.len[s];
   q.row0 = a;
   q.n = b - a;
   q.ok = a >= 0 && b >= a && b <= c.tokens && q.n <= c.max_new && q.len >= 0 && q.len <= c.max_len &&
@@ -32,7 +32,7 @@ __device__ __forceinline__ size_t block_offset(const Kv4Params& c, int page, int
 }
 // The page of a position, or -1 where the table names none of the cache.
 __device__ __forceinline__ int page_of(const Kv4Params& c, int s, int pos) {
-  const int id = __ldg(c.table + (size_t)s * c.max_pages + (pos >> c.log_page));
+  const int id = c.table[(size_t)s * c.max_pages + (pos >> c.log_page)];
   return (unsigned)id < (unsigned)c.num_pages ? id : -1;
 }
 

@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
       const int pos = b * kBlock + tid;
       ahead.valid = true;
       ahead.inside = pos < g.q.len;
-      ahead.page = ahead.inside ? __ldg(c.table + (size_t)g.s * c.max_pages + (pos >> c.log_page)) : -1;
+      ahead.page = ahead.inside ? c.table[(size_t)g.s * c.max_pages + (pos >> c.log_page)] : -1;
       ahead.slot = pos & (c.page - 1);
       ahead.h = g.h;
       ++b;
@@ -579,12 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const Kv4PromptPara
     auto load = [&](uint4 (&w)[D / 32], const Block& n, size_t off) {
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
-        w[i] = n.valid && n.there ? __ldg(reinterpret_cast<const uint4*>(n.row + off) + i) : make_uint4(0, 0, 0, 0);
+        w[i] = n.valid && n.there ? reinterpret_cast<const uint4*>(n.row + off)[i] : make_uint4(0, 0, 0, 0);
     };
     auto load_pair = [&](const Block& n) {  // the scale pairs stand behind the values, 8 bytes a token
       pair = make_uint2(0, 0);
       if (n.valid && n.there)
-        pair = __ldg(reinterpret_cast<const uint2*>(n.row - (size_t)slot * (D / 2) + p_off + (size_t)slot * 8));
+        pair = *reinterpret_cast<const uint2*>(n.row - (size_t)slot * (D / 2) + p_off + (size_t)slot * 8);
     };
     look_up();
     place(&cur);

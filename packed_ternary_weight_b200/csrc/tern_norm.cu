@@ -210,6 +210,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p
       }
     }
   };
+  // eight gains of the vector at j; a thread with one vector holds them from the start, ahead of the row's three steps (1 x
+  // 4096: 2.7 us, 2.85 us with the gains read behind the factor; with two vectors the registers are worth more)
+  float4 held[2];
+  auto gains = [&](int j, float4 (&g)[2]) {
+    const float4* src = reinterpret_cast<const float4*>(p.gain + first + j * step);
+    g[0] = src[0], g[1] = src[1];
+  };
+  if (NV == 1 && first < k) gains(0, held);
   load(blockIdx.x);
   int turn = 0;
   for (int row = blockIdx.x; row < p.m; row += gridDim.x, turn ^= 1) {
@@ -236,10 +244,13 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_row_kernel(const NormParams p
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (first + j * step < k) {
-        const float4* g = reinterpret_cast<const float4*>(p.gain + first + j * step);
-        const float4 g0 = __ldg(g), g1 = __ldg(g + 1);
-        const float2 gain[4] = {make_float2(g0.x, g0.y), make_float2(g0.z, g0.w), make_float2(g1.x, g1.y),
-                                make_float2(g1.z, g1.w)};
+        float4 g[2];
+        if (NV == 1)
+          g[0] = held[0], g[1] = held[1];
+        else
+          gains(j, g);
+        const float2 gain[4] = {make_float2(g[0].x, g[0].y), make_float2(g[0].z, g[0].w), make_float2(g[1].x, g[1].y),
+                                make_float2(g[1].z, g[1].w)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[j][e] = mul2(mul2(v[j][e], f2), gain[e]);
@@ -283,7 +294,7 @@ bool vectors(const NormParams& p) {
 }
 
 // Vectors per thread: two where there are rows enough to fill the device, one
-// where a row's latency counts (1 x 2560: 2.7 us, 6.6 us with the row read three
+// where a row's latency counts (1 x 2560: 2.4 us, 6.6 us with the row read three
 // times by 256 threads) and a block's threads suffice. About 1024 threads per
 // multiprocessor, the registers of the next row included: 8192 x 4096 with the
 // residual 62 us (0.92 of the measured copy rate; 76 us with 640 threads), 4096 x

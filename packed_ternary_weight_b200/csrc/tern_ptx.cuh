@@ -129,6 +129,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 
 // Programmatic dependent launch: wait until the preceding grid on the stream
 // has completed and its memory is visible (no-op without the launch attribute).
+// What that grid may have written is read by ordinary loads behind this: read-only
+// ones (__ldg) ask for data that nothing writes while this kernel runs, and need not
+// stay behind.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Allow the next grid on the stream to be scheduled now.
 __device__ __forceinline__ void pdl_launch_dependents() {
