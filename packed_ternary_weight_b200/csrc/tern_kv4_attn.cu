@@ -333,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!*abort && !mbar_wait_bounded(bar, parity)) *abort = 1;
   };
+  // Whether a wait of the CTA has given up, the same to all lanes of a warp: what follows takes whole warps.
+  auto gave_up = [&] { return __any_sync(0xffffffffu, *abort != 0u) != 0; };
 
   // where the warp's two groups of 16 tokens stand in a stage: their page's
   // block, then keys, values and scale pairs at the lane's token and dimensions
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
         const int stage = n % kStages;
         if (n >= kStages) wait(&sm.empty[stage], (uint32_t)(n / kStages - 1) & 1u);
         const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-        if (*abort) return;
+        if (gave_up()) return;
         if (lane == 0) {
           sm.there[stage] = there;
           sm.phase[stage] = (uint32_t)(n / kStages) & 1u;
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attn_kernel(const K
         if (duty) page = look_up(i + kStages - 1);
         wait(&sm.full[stage], (uint32_t)(use / kStages) & 1u);
         const int pos0 = begin + i * kRound + kStep * warp;
-        if (pos0 < end && !*abort) {
+        if (!gave_up() && pos0 < end) {
           const uint32_t at_stage = (uint32_t)stage * (uint32_t)sizeof(sm.ring[0]), there = sm.there[stage];
           const uint32_t kb[2] = {okb[0] + at_stage, okb[1] + at_stage}, vb[2] = {ovb[0] + at_stage, ovb[1] + at_stage},
                          pb[2] = {opb[0] + at_stage, opb[1] + at_stage};
