@@ -504,6 +504,8 @@ class KV4Cache:
         bf16 = _torch.bfloat16
         _vector(q, batch.tokens * heads * self.head_dim, bf16, "tern_kv4_attention: q")
         _vector(out, batch.tokens * width, bf16, "tern_kv4_attention: out")
+        if ws is not None and not ws.is_contiguous():
+            _bad(f"{what}: the workspace is not contiguous")
         if batch.dev != dev or q.get_device() != dev or out.get_device() != dev or (ws is not None and ws.get_device() != dev):
             _bad(f"{what}: tensors on several devices")
         _launch(dev, stream, what, lib.tern_kv4_attention, self._ref, batch._ref, heads, scale, q.data_ptr(),
