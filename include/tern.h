@@ -263,8 +263,8 @@ tern_status tern_stream_read(const void* d_src, size_t bytes, int32_t mode, int3
  * Read and clear the device error word (synchronises `stream`).
  * Returns TERN_OK if no kernel reported a failure, TERN_ETIMEOUT if a bounded
  * wait expired, TERN_EFORMAT if a kernel met packed data it cannot use (the
- * tensor path: a header scale-digit count outside 1..6), TERN_ECUDA if the
- * read failed.
+ * tensor path: a header scale-digit count outside 1..6) or a tern_kv4_batch that
+ * cannot be right, TERN_ECUDA if the read failed.
  */
 tern_status tern_device_error(void* stream);
 

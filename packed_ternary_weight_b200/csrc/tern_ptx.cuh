@@ -17,10 +17,14 @@ static __device__ unsigned int g_dev_error = 0;
 
 static inline int read_clear_dev_error_tu(void* stream, unsigned* out) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  unsigned v = 0, zero = 0;
+  unsigned v = 0;
+  const unsigned zero = 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_dev_error, sizeof(v), 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_dev_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v != 0) {  // a word that is clear, nearly always, costs one copy
+    e = cudaMemcpyToSymbolAsync(g_dev_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
   *out |= v;
   return (int)e;
 }
