@@ -443,7 +443,8 @@ typedef struct tern_kv4_cache {
  * than max_new new tokens, a length above max_len or above what its table
  * holds) is left out: nothing of it is stored and its outputs are not written.
  * The tokens of a page outside the cache are left out: not stored, not attended
- * to, read as zero. Both are reported by tern_device_error as TERN_EFORMAT.
+ * to, read as zero. Both are reported by tern_device_error as TERN_EFORMAT. Where
+ * d_start descends, append and read may leave out rows of other sequences too.
  */
 typedef struct tern_kv4_batch {
   int32_t seqs;            /* sequences, 0 .. 65535 */
@@ -501,8 +502,9 @@ tern_status tern_kv4_attention_workspace_size(const tern_kv4_cache* cache, int32
  * below 2^-127 excepted). Sequences with up
  * to 48 new tokens x heads per kv head multiply by the codes, which are exact, and round
  * probabilities times value scales to fp16; longer ones round keys, values and
- * probabilities to fp16. Scores must be finite in fp32, and scale times any element
- * of q below 2^117.
+ * probabilities to fp16. A batch of one sequence is taken by its bound, the smaller of
+ * max_new and tokens: above 48 x kv_heads / heads it counts as longer whatever its rows.
+ * Scores must be finite in fp32, and scale times any element of q below 2^117.
  *   d_q, d_out bf16 [tokens][heads * head_dim], 16-byte aligned; d_out may be d_q.
  */
 tern_status tern_kv4_attention(const tern_kv4_cache* cache, const tern_kv4_batch* batch, int32_t heads, float scale,

@@ -711,7 +711,8 @@ extern "C" tern_status tern_kv4_attention(const tern_kv4_cache* cache, const ter
   if (!d_q || !d_out) return TERN_EINVAL;
   if (((reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_out)) & 15u) != 0) return TERN_EALIGN;
   Plan pl{};
-  st = plan_attn(p.c, heads, p.c.seqs, p.c.max_new, p.c.max_len, sm_count(), &pl);
+  // no sequence has more new tokens than the buffers have rows, however generous the bound is
+  st = plan_attn(p.c, heads, p.c.seqs, std::min(p.c.max_new, p.c.tokens), p.c.max_len, sm_count(), &pl);
   if (st != TERN_OK) return st;
   if (pl.total > 0) {
     if (!d_ws || ws_bytes < pl.total) return TERN_ENOSPACE;

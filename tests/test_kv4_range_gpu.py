@@ -69,3 +69,40 @@ def test_roundings_of_the_weights_cancel_in_the_offset(tern, new, d, length):
     q, got = attend(tern, b, heads, math.log(2.0), q)
     ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, heads, math.log(2.0), q)
     assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,group", [(17, 1), (8, 4), (11, 3), (12, 4), (2, 8), (1, 5)])
+@pytest.mark.parametrize("offset", [0.0, 6.0])
+def test_one_sequence_of_few_rows(tern, d, new, group, offset):
+    # up to 48 query rows of a single sequence multiply by the codes, and are held to that kernel's bound
+    b = util().Batch([new], [300 + new], 2, d, 32, seed=43 + new)
+    c = b.oracle_cache()
+    for j in range(int(b.len[0])):
+        for h in range(2):
+            for w in range(2):
+                codes, s, m = prompt.quantize4((b.g.standard_normal((1, d)) + w * offset).astype(np.float32))
+                c.put(int(b.table[0, j // 32]), j % 32, h, w, codes[0], s[0], m[0])
+    heads = 2 * group
+    q, got = attend(tern, b, heads, d ** -0.5, b.g.standard_normal((new, heads, d)))
+    ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, heads, d ** -0.5, q)
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("new,bound", [(1, 400), (3, 4000)])
+def test_a_generous_bound_does_not_choose_the_kernel(tern, new, bound):
+    # the buffers have few rows: the result is that of the exact bound
+    b = util().Batch([new], [900], 2, 64, 16, seed=44)
+    b.fill_values()
+    q = b.g.standard_normal((new, 8, 64))
+    want, got = attend(tern, b, 8, 0.125, q)[1], attend(tern, b, 8, 0.125, q, max_new=bound)[1]
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("new,length", [([16], [3500]), ([13, 20], [3000, 2500])])
+def test_cut_prompts_of_wide_heads(tern, new, length):
+    # few rows and long histories at D = 128: one tile's blocks go to several CTAs, whose parts are joined
+    b = util().Batch(new, length, 1, 128, 64, seed=45)
+    b.fill_values()
+    q, got = attend(tern, b, 4, 128 ** -0.5, b.g.standard_normal((b.rows, 4, 128)))
+    ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, 4, 128 ** -0.5, q)
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
