@@ -420,8 +420,8 @@ tern_status tern_norm_quantize(tern_norm mode, int32_t m, int32_t k, tern_out x_
  * token and head has its own scales, for keys (after RoPE) and for values x:
  *   min = fp16_rn(min x), scale = fp16_rn(fl(fl(max x - min x) / 15)),
  *   code = clamp(rint(fl(fl(x - min) fl(1 / scale))), 0, 15); scale 0: code 0.
- * Values must be finite and within +-65000: what the codes stand for, min + 15 scale
- * at most, then stays in the fp16 range.
+ * Values must be within +-65000: what the codes stand for, min + 15 scale at most, then
+ * stays in the fp16 range. A head with a value that is not finite reads as not finite.
  */
 typedef struct tern_kv4_cache {
   int32_t kv_heads;   /* 1..1024 */

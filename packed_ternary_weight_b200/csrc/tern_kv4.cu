@@ -84,6 +84,18 @@ __device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
 }
 
+// The smaller and the larger one, not a number if either is not: a head's scales must show what stands in it.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 constexpr int kMaxHeads = 3;  // of a token that a group of lanes takes
 
 // A warp's token and the heads of its groups: first, first + step, .. (count of them, the same in both groups).
@@ -175,11 +187,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Kv4AppendParams 
     if (__all_sync(0xffffffffu, is_q || g >= total)) continue;
     float mn = a[0], mx = a[0];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mn = fminf(mn, fminf(a[k], b[k])), mx = fmaxf(mx, fmaxf(a[k], b[k]));
+    for (int k = 0; k < 8; ++k) mn = min_nan(mn, min_nan(a[k], b[k])), mx = max_nan(mx, max_nan(a[k], b[k]));
 #pragma unroll
     for (int o = Place<D>::L / 2; o; o >>= 1) {
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
     if (is_q || g >= total || page < 0) continue;
     const int head = is_k ? g - c.heads : g - c.heads - c.kv_heads;

@@ -106,3 +106,47 @@ def test_cut_prompts_of_wide_heads(tern, new, length):
     q, got = attend(tern, b, 4, 128 ** -0.5, b.g.standard_normal((b.rows, 4, 128)))
     ref, tol = prompt.attention(b.oracle_cache(), b.table, b.start, b.len, 4, 128 ** -0.5, q)
     assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d,n", [(64, 5), (128, 900)])        # one head per group of lanes; several
+def test_appended_values_that_are_not_finite_show(tern, bad, dt, d, n):
+    # a key head or value head with a value that the cache cannot hold reads as not finite; all others are as without it
+    u, kvh, heads = util(), 2, 6
+    b = u.Batch([n], [n], kvh, d, 16, seed=46)
+    k, v, q = (torch.from_numpy(b.g.standard_normal((n, h * d)).astype(np.float32)).to(dt).cuda() for h in (kvh, kvh, heads))
+    rope = torch.from_numpy(tern.decode_rope_table(n, d)).cuda()
+    cache, batch = b.device()
+    qo = torch.empty((n, heads * d), dtype=torch.bfloat16, device="cuda")
+    res = []
+    for _ in range(2):
+        cache.append(batch, q, k, v, rope, qo)
+        ko, vo = torch.empty((n, kvh * d), device="cuda"), torch.empty((n, kvh * d), device="cuda")
+        cache.read(batch, ko, vo)
+        res.append((ko.view(n, kvh, d), vo.view(n, kvh, d)))
+        k[1, 7], v[3, d + 9] = float(bad), float(bad)        # token 1's first key head, token 3's second value head
+    (k0, v0), (k1, v1) = res
+    assert not k1[1, 0].isfinite().any() and not v1[3, 1].isfinite().any()
+    k1[1, 0], v1[3, 1] = k0[1, 0], v0[3, 1]
+    assert torch.equal(k0, k1) and torch.equal(v0, v1)
+    out = torch.empty_like(qo)
+    cache.attention(batch, qo, d ** -0.5, out, u.workspace(cache, heads, 1, n, n))
+    o = out.view(n, kvh, 3, d)
+    assert o[:3, 1].isfinite().all() and not o[3:, 1].isfinite().any()     # values of the second head, from token 3 on
+    assert o[:1, 0].isfinite().all()
+    if bad == "nan":
+        assert not o[1:, 0].isfinite().any()                               # keys of the first, from token 1 on
+    assert tern.device_error() == tern.OK
+
+
+def test_a_query_that_is_not_a_number_in_a_prompt(tern):
+    b = util().Batch([60], [300], 1, 64, 16, seed=47)
+    b.fill_values()
+    q = b.g.standard_normal((60, 2, 64))
+    want = attend(tern, b, 2, 0.125, q)[1]
+    q[7, 1, 5], q[9, 0, 3] = float("nan"), float("inf")
+    got = attend(tern, b, 2, 0.125, q)[1]
+    assert not np.isfinite(got[7, 1]).any() and not np.isfinite(got[9, 0]).any()
+    got[7, 1], got[9, 0] = want[7, 1], want[9, 0]
+    assert np.array_equal(got, want)
