@@ -19,9 +19,10 @@
 // Enough tiles for every pair of SMs: pairs of CTAs (cta_group::2) take 256
 // channels by up to 256 tokens, each loading its own 128 channels and half of the
 // tokens, which is 32 KB instead of 48 KB per SM and step (one CTA per tile was
-// held up by these loads: tensor pipe 67 % active, 75 % with pairs). 4095 x 14336 x
-// 4096 then takes 196 us, 2.46 POP/s; a
-// token's 65536 x 2560 head 31 us, 5.5 TB/s (0.85 of the measured copy rate).
+// held up by these loads: tensor pipe 67 % active, 74 % with pairs). 4095 x 14336 x
+// 4096 then takes 195-205 us in a replayed graph, 2.4 POP/s (213 us over seconds, at the
+// power cap's 1.44 GHz); a token's 65536 x 2560 head 31 us, 5.5 TB/s (0.85 of the
+// measured copy rate).
 // Fewer tiles than SMs: the steps of a tile are dealt to a cluster of up to eight
 // CTAs, whose exact int32 partial sums meet in distributed shared memory; each
 // CTA of the cluster finishes a share of the tokens. Integer sums: the result
@@ -355,7 +356,7 @@ const int* resident_clusters(int sms) {
 // two waves, 19 us; the fewest tiles, 8 of 256, 27 us. 4095 x 2560 x 2560 33 and 40 us.
 // Constants from 64 to 160 differ by 3 %). Pairs of CTAs from one 256-channel tile
 // per pair of SMs on and with wide tiles (256 x 32768 x 2560: pairs 31.5, single CTAs
-// 33.4 us; 4095 x 14336 x 4096 202 and 220; 128 x 32768 x 2560 22.7 and 21.7).
+// 33.4 us; 4095 x 14336 x 4096 8 % less than single CTAs; 128 x 32768 x 2560 22.7 and 21.7).
 // Fewer tiles than half the SMs: the fewest, and K split over a cluster, as long as
 // every CTA keeps four steps; of the cluster sizes the one with the least steps in a
 // row, where meeting costs about four (61 x 2560 x 6912: 7 us, unsplit 16 us).

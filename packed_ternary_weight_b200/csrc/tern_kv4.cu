@@ -10,8 +10,9 @@
 // shuffles. A warp takes one head per group of a few tokens and up to three of each
 // of many: the search for the token's sequence, its rotation row and its page are
 // then shared by them, and the heads' loads are issued together, ahead of that search.
-// 8813 prompt tokens (32 heads on 8 kv heads, D = 128, bf16): append 40 us, 3.9 TB/s,
-// bound by instruction issue (59 % of the slots) next to memory; read 13.5 us.
+// 8813 prompt tokens (32 heads on 8 kv heads, D = 128, bf16): append 41 us, 4.8 TB/s of
+// the bytes it has to move (0.74 of the measured copy rate), with 60 % of the issue slots
+// in use; read 13.5 us, the integer pipe at 65 % (codes to fp32: shift, mask, conversion).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -38,10 +38,11 @@
 // Memory. A page's block of one head is contiguous, so a round of 256 positions
 // arrives in 256 / page_size bulk copies, into a ring of three stages of a round
 // each; two CTAs per multiprocessor keep 139 KB in flight. The warp that requests a
-// round changes with every round. The kernel is bound by its bit operations
-// (masks, shifts and byte permutations run at half the issue rate: about 90 of
-// them per lane and 16 tokens), so rounds that every row sees as a whole take a
-// path without masks.
+// round changes with every round. Neither memory nor a pipe is full (64 sequences up
+// to 8192: DRAM 42 %, issue 55 %, integer pipe 49 % with about 90 masks, shifts and byte
+// permutations per lane and 16 tokens): sixteen warps per multiprocessor do not hide
+// the latencies of a step, which is one chain from scores to weights to values. Rounds
+// that every row sees as a whole take a path without masks.
 //
 // Split. The work is one line of rounds, 256 positions of a (sequence, kv head,
 // tile of query rows), laid end to end over the whole batch; CTA c of G takes
@@ -53,10 +54,12 @@
 // holds at most one tile that it begins and does not end and one that it ends
 // or passes through, so two slots of the workspace per CTA are enough.
 //
-// Measured (D = 128, heads : kv heads = 4): one token of 64 sequences of up to 8192
-// positions 57 us, 3.8 TB/s (0.59 of the measured copy rate); of one sequence of 131072
-// 39 us, 3.6 TB/s; of one of 1024 8.5 us, mostly the fixed part: launch, search, the latency
-// of page table and pages, join.
+// Measured (D = 128, heads : kv heads = 4; device times of replayed graphs, a call through
+// the binding takes up to 1 us more): one token of 64 sequences of up to 8192 positions 58
+// us, 3.7 TB/s (0.58 of the measured copy rate); of one sequence of 131072 40 us, 3.6
+// TB/s; of one of 1024 8.5 us, mostly the fixed part: launch, search, the latency of page
+// table and pages, join. Sixteen rows (64 x 4000 positions, 4 tokens of 4 heads): 38 us, 1.8
+// TB/s, with 242 registers and one CTA of eight warps per multiprocessor.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -631,8 +634,8 @@ int launch_one(const Kv4AttnParams& p, int ctas, cudaStream_t s) {
 // (up to three tiles that read the codes anew, from L2); longer ones the prompt
 // kernel, whose time does not depend on the rows up to 256. At D = 128 with two kv
 // heads, this kernel with 16 / 32 / 48 rows and the prompt kernel: 64 sequences of
-// 4000 positions 38 / 61 / 85 and 94 us, one of 30000 23 / 23 / 26 and 59 us, 8 of 1000
-// 13 / 13 / 19 and 26 us; a fourth tile would lose.
+// 4000 positions 38 / 63 / 87 and 94 us, one of 30000 23 / 23 / 26 and 59 us, 8 of 1000
+// 14 / 14 / 19 and 26 us; a fourth tile would lose.
 // Workspace: the CTAs' counters of both kernels, then their parts, at places that
 // only the device and the cache's shape decide, so that batches of any size share it.
 struct Plan {

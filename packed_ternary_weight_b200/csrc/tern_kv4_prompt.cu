@@ -34,7 +34,12 @@
 // between CTAs is joined by the last of them, in position order.
 //
 // Measured: 2048-token chunks behind 6142 positions and shorter ones (32 heads on 8 kv
-// heads, D = 128) 0.43 ms, 0.88 PFLOP/s, half of the measured bf16 rate. A block of both
+// heads, D = 128) 0.44-0.45 ms in a replayed graph, 0.85 PFLOP/s, half of the measured bf16
+// rate (0.46 ms as calls; 0.47 ms over seconds, at the power cap's 1.79 GHz); the same at D
+// = 64 0.33 ms (the exponentials are the same, the products half). A unit of one block
+// takes 9 us by itself, so a prompt of 2048 without history takes 140 us, as long as one
+// behind 2048 positions: shares count blocks, and the first tiles, of one or two blocks
+// each, go to a few CTAs. A block of both
 // tiles takes about 4800 cycles, 2050 of them of tensor work at the full rate; the limit is
 // each tile's own chain, which nothing shortens by overlap: softmax 2700 (its exponentials
 // alone 2050 of the special-function pipe, shared with the other tile), O += P V and the

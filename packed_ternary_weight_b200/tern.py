@@ -497,7 +497,7 @@ class KV4Cache:
 
     def attention(self, batch: KV4Batch, q, scale: float, out, ws=None, stream=None):
         """Causal attention of the batch's new tokens over the cache: q, out bfloat16 [tokens][heads * head_dim]
-        contiguous (out may be q); ws uint8, zero before its first use (attention_workspace_size)."""
+        contiguous (out may be q); ws uint8, contiguous, zero before its first use (attention_workspace_size)."""
         what = "tern_kv4_attention"
         width, dev = q.shape[-1], self.dev
         heads = width // self.head_dim
